@@ -21,6 +21,9 @@ ERR_INVALID_ARG = 1
 ERR_UNSUPPORTED = 2
 ERR_CUDA = 3
 ERR_TIMEOUT = 4
+ERR_PAGE = 5
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
 
 EXPORTS = (
     "streamkl_fwd",
@@ -40,9 +43,21 @@ EXPORTS = (
     "streamkl_num_sms",
     "streamkl_probe_clock",
     "streamkl_eval_exp2",
+    "streamkl_cache_append",
+    "streamkl_cache_gather",
+    "streamkl_paged_workspace_bytes",
+    "streamkl_paged_attn",
+    "streamkl_paged_kl",
 )
 
 _lib = None
+
+
+class CacheStruct(ctypes.Structure):
+    """streamkl_cache of the header."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("type", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int)]
 
 
 class StreamKLError(RuntimeError):
@@ -101,6 +116,16 @@ def load(path=None):
     lib.streamkl_probe_clock.restype = i
     lib.streamkl_eval_exp2.argtypes = [i, vp, vp, ctypes.c_longlong, vp]
     lib.streamkl_eval_exp2.restype = i
+    lib.streamkl_cache_append.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, vp]
+    lib.streamkl_cache_append.restype = i
+    lib.streamkl_cache_gather.argtypes = [vp, vp, i, vp, vp, i, i, vp, vp, vp]
+    lib.streamkl_cache_gather.restype = i
+    lib.streamkl_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.streamkl_paged_workspace_bytes.restype = sz
+    lib.streamkl_paged_attn.argtypes = [vp, vp, vp, i, vp, i, i, i, f, i, vp, vp, vp, sz, vp]
+    lib.streamkl_paged_attn.restype = i
+    lib.streamkl_paged_kl.argtypes = [vp, vp, vp, vp, vp, i, vp, i, i, i, f, i, vp, vp, vp, vp, sz, vp]
+    lib.streamkl_paged_kl.restype = i
     if path is None:
         _lib = lib
     return lib
@@ -225,6 +250,42 @@ def streamkl_eval_exp2(kind, x, stream=None):
     y = torch.empty_like(x)
     rc = load().streamkl_eval_exp2(int(kind), _ptr(x), _ptr(y), x.numel(), _stream(stream))
     return rc, y
+
+
+def _cache_ref(cache):
+    """A pointer to the streamkl_cache of a PagedCache or CacheStruct (None stays NULL)."""
+    if cache is None:
+        return None
+    return ctypes.byref(cache.struct if isinstance(cache, PagedCache) else cache)
+
+
+def streamkl_cache_append(cache, k, v, table, width, start, count, B, NT, stream=None):
+    return load().streamkl_cache_append(_cache_ref(cache), _ptr(k), _ptr(v), _ptr(table), width, _ptr(start),
+                                        _ptr(count), B, NT, _stream(stream))
+
+
+def streamkl_cache_gather(cache, table, width, start, count, B, NT, k, v, stream=None):
+    return load().streamkl_cache_gather(_cache_ref(cache), _ptr(table), width, _ptr(start), _ptr(count), B, NT,
+                                        _ptr(k), _ptr(v), _stream(stream))
+
+
+def streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d):
+    return load().streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d)
+
+
+def streamkl_paged_attn(cache, q, table, width, lengths, B, Hq, NQ, scale, causal, out, lse, workspace,
+                        workspace_bytes, stream=None):
+    return load().streamkl_paged_attn(_cache_ref(cache), _ptr(q), _ptr(table), width, _ptr(lengths), B, Hq, NQ,
+                                      float(scale), int(bool(causal)), _ptr(out), _ptr(lse), _ptr(workspace),
+                                      int(workspace_bytes), _stream(stream))
+
+
+def streamkl_paged_kl(cache1, q1, cache2, q2, table, width, lengths, B, Hq, NQ, scale, causal, kl, lse1, lse2,
+                      workspace, workspace_bytes, stream=None):
+    return load().streamkl_paged_kl(_cache_ref(cache1), _ptr(q1), _cache_ref(cache2), _ptr(q2), _ptr(table), width,
+                                    _ptr(lengths), B, Hq, NQ, float(scale), int(bool(causal)), _ptr(kl),
+                                    _ptr(lse1), _ptr(lse2), _ptr(workspace), int(workspace_bytes),
+                                    _stream(stream))
 
 
 def status_string(status):
@@ -363,4 +424,241 @@ def bwd(mode, q1, k1, q2, k2, kl, lse1, lse2, dkl, scale=None, causal=False, out
                       stream=stream)
     if rc != OK:
         raise StreamKLError(rc, "streamkl_bwd")
+    return out
+
+
+# ------------------------------------------------------------------ paged key-value cache
+class PagedCache:
+    """The pages of a key-value cache: k and v [pages, Hkv, page_size, d], bf16 or float8_e4m3fn; with
+    e4m3, k_exp and v_exp uint8 [pages, Hkv, page_size] (a row's scale is 2^(byte - 127)).  v may be
+    None for a cache that only paged_kl reads.  Holds the tensors and the C struct that points to
+    them; page tables, lengths and positions are the caller's int32 tensors."""
+
+    def __init__(self, k, v=None, k_exp=None, v_exp=None):
+        import torch
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not k.is_cuda:
+            raise ValueError("k must be a bf16 or float8_e4m3fn CUDA tensor [pages, Hkv, page_size, d]")
+        quantised = k.dtype == torch.float8_e4m3fn
+        rows = tuple(k.shape[:3])
+        _check_tensor("k", k, k.shape, k.dtype, k.device)
+        if v is not None:
+            _check_tensor("v", v, k.shape, k.dtype, k.device)
+        if quantised:
+            _check_tensor("k_exp", k_exp, rows, torch.uint8, k.device)
+            if v is not None:
+                _check_tensor("v_exp", v_exp, rows, torch.uint8, k.device)
+        elif k_exp is not None or v_exp is not None:
+            raise ValueError("a bf16 cache has no scales")
+        pages, Hkv, page_size, d = k.shape
+        if d not in (64, 128) or page_size not in (16, 32, 64, 128, 256, 512, 1024) or pages < 1 or Hkv < 1:
+            raise ValueError("pages of 16 to 1024 rows (a power of two) and d = 64 or 128 are supported (got %s)"
+                             % (tuple(k.shape),))
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.shape = (pages, Hkv, page_size, d)
+        self.device = k.device
+        self.struct = CacheStruct(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp),
+                                  CACHE_E4M3 if quantised else CACHE_BF16, pages, page_size, Hkv, d)
+
+    @classmethod
+    def empty(cls, pages, Hkv, page_size, d, quantised=False, values=True, device="cuda"):
+        """A cache of zeros."""
+        import torch
+        dtype = torch.float8_e4m3fn if quantised else torch.bfloat16
+        n = 2 if values else 1
+        rows = [torch.zeros((pages, Hkv, page_size, d), dtype=torch.uint8 if quantised else dtype,
+                            device=device).view(dtype) for _ in range(n)]
+        exps = [torch.full((pages, Hkv, page_size), 127, dtype=torch.uint8, device=device) if quantised else None
+                for _ in range(n)]
+        return cls(rows[0], rows[1] if values else None, exps[0], exps[1] if values else None)
+
+
+def paged_workspace(B, Hq, Hkv, NQ, d, device="cuda"):
+    """A workspace for paged_attn and paged_kl of these sizes, to be kept between calls."""
+    import torch
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        nbytes = streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d)
+    if nbytes == 0:
+        raise ValueError("unsupported sizes: B %d, Hq %d, Hkv %d, NQ %d, d %d" % (B, Hq, Hkv, NQ, d))
+    return torch.empty(nbytes // 4, dtype=torch.float32, device=device)
+
+
+def _enter(device, stream):
+    """(guard, stream handle) of a call on `device`: what the call allocates belongs to the stream it
+    runs on, the caller's `stream` (an object or a handle) or the device's current one."""
+    import torch
+    if stream is None:
+        guard = None
+        if device.index != torch.cuda.current_device():
+            guard = torch.cuda.device(device)
+            guard.__enter__()
+        return guard, torch._C._cuda_getCurrentRawStream(device.index)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, device))
+    guard = torch.cuda.stream(stream)
+    guard.__enter__()
+    return guard, stream.cuda_stream
+
+
+def _leave(guard):
+    if guard is not None:
+        guard.__exit__(None, None, None)
+
+
+def _check_ints(name, t, shape, device):
+    import torch
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s (got %s %s on %s)"
+                         % (name, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+
+
+def _check_paging(cache, table, B):
+    if table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be int32 [B, width]")
+    _check_ints("table", table, (B, table.shape[1]), cache.device)
+
+
+def _check_rows(cache, k, v):
+    import torch
+    if cache.v is None:
+        raise ValueError("this cache has no values")
+    if k.dim() != 4 or k.shape[1] != cache.shape[1] or k.shape[3] != cache.shape[3] or k.shape[0] < 1 or k.shape[2] < 1:
+        raise ValueError("k and v must be [B, %d, rows, %d] (got %s)" % (cache.shape[1], cache.shape[3], tuple(k.shape)))
+    _check_tensor("k", k, k.shape, torch.bfloat16, cache.device)
+    _check_tensor("v", v, k.shape, torch.bfloat16, cache.device)
+
+
+def cache_append(cache, k, v, table, start, count=None, stream=None):
+    """Writes k, v (bf16 [B, Hkv, NT, d]) into the cache: row i < count[b] (NT without `count`) of
+    sequence b at position start[b] + i.  table int32 [B, width], start and count int32 [B]."""
+    _check_rows(cache, k, v)
+    B, _, NT, _ = k.shape
+    _check_paging(cache, table, B)
+    _check_ints("start", start, (B,), cache.device)
+    if count is not None:
+        _check_ints("count", count, (B,), cache.device)
+    guard, handle = _enter(cache.device, stream)
+    try:
+        rc = load().streamkl_cache_append(ctypes.byref(cache.struct), k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                                          table.shape[1], start.data_ptr(), _ptr(count), B, NT, handle)
+    finally:
+        _leave(guard)
+    if rc != OK:
+        raise StreamKLError(rc, "streamkl_cache_append")
+
+
+def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=None):
+    """Reads rows back into (k, v), bf16 [B, Hkv, rows, d]: row i < count[b] is the cached row at position
+    start[b] + i (from 0 without `start`); rows behind the count are left as they were (zeros in
+    tensors allocated here)."""
+    import torch
+    if out is None and (rows is None or rows < 1 or table.dim() != 2):
+        raise ValueError("out, or rows of at least 1 and a table [B, width], are required")
+    guard, handle = _enter(cache.device, stream)
+    try:
+        if out is None:
+            out = tuple(torch.zeros((table.shape[0], cache.shape[1], rows, cache.shape[3]), dtype=torch.bfloat16,
+                                    device=cache.device) for _ in range(2))
+        k, v = out
+        _check_rows(cache, k, v)
+        if rows is not None and rows != k.shape[2]:
+            raise ValueError("out has %d rows, not %d" % (k.shape[2], rows))
+        B = k.shape[0]
+        _check_paging(cache, table, B)
+        _check_ints("count", count, (B,), cache.device)
+        if start is not None:
+            _check_ints("start", start, (B,), cache.device)
+        rc = load().streamkl_cache_gather(ctypes.byref(cache.struct), table.data_ptr(), table.shape[1], _ptr(start),
+                                          count.data_ptr(), B, k.shape[2], k.data_ptr(), v.data_ptr(), handle)
+    finally:
+        _leave(guard)
+    if rc != OK:
+        raise StreamKLError(rc, "streamkl_cache_gather")
+    return out
+
+
+def _check_paged(cache, q, table, lengths):
+    import torch
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.shape[3] or min(shape) < 1 or shape[1] % cache.shape[1]:
+        raise ValueError("q must be [B, Hq, NQ, %d], Hq a multiple of %d (got %s)"
+                         % (cache.shape[3], cache.shape[1], tuple(shape)))
+    if q.dtype is not torch.bfloat16 or q.device != cache.device or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor on %s" % (cache.device,))
+    _check_paging(cache, table, shape[0])
+    _check_ints("lengths", lengths, (shape[0],), cache.device)
+
+
+def _paged_scratch(workspace, B, Hq, Hkv, NQ, d, device):
+    import torch
+    need = load().streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d)
+    if workspace is None:
+        return torch.empty(need // 4, dtype=torch.float32, device=device)
+    _check_workspace(workspace, need, device)
+    return workspace
+
+
+def paged_attn(q, cache, table, lengths, scale=None, causal=True, out=None, workspace=None, stream=None):
+    """Attention of new tokens over the cache: (out bf16 [B, Hq, NQ, d], lse fp32 [B, Hq, NQ]).  lengths int32
+    [B] count the new tokens; causal: they are the last NQ and see their own past only.  `workspace`
+    (paged_workspace) is allocated here when not given."""
+    import torch
+    _check_paged(cache, q, table, lengths)
+    if cache.v is None:
+        raise ValueError("this cache has no values")
+    B, Hq, NQ, d = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    guard, handle = _enter(q.device, stream)
+    try:
+        if out is None:
+            out = (torch.empty_like(q), torch.empty((B, Hq, NQ), dtype=torch.float32, device=q.device))
+        else:
+            _check_tensor("out", out[0], q.shape, torch.bfloat16, q.device)
+            _check_tensor("lse", out[1], (B, Hq, NQ), torch.float32, q.device)
+        workspace = _paged_scratch(workspace, B, Hq, cache.shape[1], NQ, d, q.device)
+        rc = load().streamkl_paged_attn(ctypes.byref(cache.struct), q.data_ptr(), table.data_ptr(), table.shape[1],
+                                        lengths.data_ptr(), B, Hq, NQ, scale, 1 if causal else 0,
+                                        out[0].data_ptr(), out[1].data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), handle)
+    finally:
+        _leave(guard)
+    if rc != OK:
+        raise StreamKLError(rc, "streamkl_paged_attn")
+    return out
+
+
+def paged_kl(q1, cache1, q2, cache2, table, lengths, scale=None, causal=True, out=None, workspace=None, stream=None):
+    """KL(P1 || P2) of two attentions of the new tokens over paged key caches: (kl, lse1, lse2), fp32
+    [B, Hq, NQ].  P1 from q1 and cache1's keys, P2 from q2 and cache2's; pass the same cache twice
+    for shared keys.  Other arguments as paged_attn."""
+    import torch
+    _check_paged(cache1, q1, table, lengths)
+    if q1.shape != q2.shape or cache1.shape != cache2.shape or cache1.device != cache2.device:
+        raise ValueError("both sides must agree in shape and device (q %s and %s, caches %s and %s)"
+                         % (tuple(q1.shape), tuple(q2.shape), cache1.shape, cache2.shape))
+    if q2.dtype is not torch.bfloat16 or q2.device != q1.device or not q2.is_contiguous():
+        raise ValueError("q2 must be a contiguous bf16 tensor on %s" % (q1.device,))
+    B, Hq, NQ, d = q1.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    guard, handle = _enter(q1.device, stream)
+    try:
+        if out is None:
+            out = tuple(torch.empty((B, Hq, NQ), dtype=torch.float32, device=q1.device) for _ in range(3))
+        else:
+            for name, o in zip(("kl", "lse1", "lse2"), out):
+                _check_tensor(name, o, (B, Hq, NQ), torch.float32, q1.device)
+        workspace = _paged_scratch(workspace, B, Hq, cache1.shape[1], NQ, d, q1.device)
+        rc = load().streamkl_paged_kl(ctypes.byref(cache1.struct), q1.data_ptr(), ctypes.byref(cache2.struct),
+                                      q2.data_ptr(), table.data_ptr(), table.shape[1], lengths.data_ptr(), B, Hq, NQ,
+                                      scale, 1 if causal else 0, out[0].data_ptr(), out[1].data_ptr(),
+                                      out[2].data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle)
+    finally:
+        _leave(guard)
+    if rc != OK:
+        raise StreamKLError(rc, "streamkl_paged_kl")
     return out

@@ -1,0 +1,300 @@
+// paged.cuh -- what the kernels over a paged key-value cache share: the cache's view, the
+// division of the work among a persistent grid, and the warp-level pieces (asynchronous copies
+// into lane-private shared memory, the m16n8k16 product, e4m3 rows).
+//
+// A cache pool holds pages of one kind of row (keys or values), [pages, Hkv, page_size, d],
+// bf16 or e4m3; an e4m3 row has one power-of-two scale, kept as the byte exponent + 127 in
+// [pages, Hkv, page_size].  Sequence b's token j lies in page table[b][j / page_size].
+//
+// Work division.  A segment is one (sequence, KV head, block of query rows); its keys are cut
+// into units of 64.  All segments' units in a row, T of them, are dealt out in equal contiguous
+// shares of P = ceil(T / grid): lengths are read on the device, so a ragged batch loads every
+// SM alike and the host needs no lengths.  A share may begin or end inside a segment; such a
+// CTA stores a partial state, and a second kernel joins the partial states of a segment in
+// the order of its CTAs (no atomics: the same inputs give the same bits).  A CTA has at most two
+// partial segments, its first (slot 2c) and its last (slot 2c + 1), so the workspace depends on
+// the grid alone and not on the lengths.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace skl {
+
+// A page table entry or a length that points outside the cache (STREAMKL_ERR_PAGE, 5).  A word of
+// its own: the pipelined kernels give up their waits when g_status is set.
+__device__ int g_page_status = 0;
+
+constexpr int kPagedThreads = 128;     // 4 warps, each with its own tiles and copies
+constexpr int kPagedWarps = kPagedThreads / 32;
+constexpr int kTileKeys = 16;          // keys a warp folds at a time (the product's M)
+constexpr int kUnitKeys = kPagedWarps * kTileKeys;
+constexpr float kNoMax = -3.402823466e38f;   // running maximum before any key
+
+struct PagedPool {
+    const uint8_t* rows;
+    const uint8_t* exps;   // nullptr for bf16
+};
+
+struct PagedParams {
+    PagedPool a, b;        // attention: keys, values; divergence: keys 1, keys 2
+    const int* table;      // [B, width]
+    const int* lengths;    // [B]
+    const uint16_t* q1;    // [B, Hq, NQ, d]: the rows of one KV head are contiguous
+    const uint16_t* q2;
+    int B, Hkv, NQ;
+    int rows;              // query rows of one KV head: Hq / Hkv * NQ
+    int rblocks;           // blocks of query rows
+    int width, pages, page_size, page_shift;
+    int causal;
+    int min_units;         // least share of a CTA
+    int grid;              // CTAs of the main kernel
+    float sl2;             // scale * log2(e)
+    uint16_t* out;         // attention
+    float* lse1;
+    float* lse2;           // divergence
+    float* kl;
+    float* part;           // partial states, slot-major
+};
+
+__device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
+    const int n = p.lengths[b];
+    const int cap = p.width * p.page_size;
+    return n < 0 ? 0 : (n > cap ? cap : n);
+}
+
+__device__ __forceinline__ int seq_units(const PagedParams& p, int b) {
+    return (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+}
+
+// Sum of x over the CTA's 128 threads, in every thread.  red: 4 ints.
+__device__ __forceinline__ int block_sum(int x, int* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];
+}
+
+// T: units of all segments.
+__device__ __forceinline__ int plan_total(const PagedParams& p, int* red) {
+    int n = 0;
+    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) n += seq_units(p, b);
+    return block_sum(n, red) * p.Hkv * p.rblocks;
+}
+
+// The share of a CTA.
+__device__ __forceinline__ int plan_share(const PagedParams& p, int total) {
+    return max((total + p.grid - 1) / p.grid, p.min_units);
+}
+
+// The sequence that holds unit g (0 <= g < T), and the first unit of that sequence.
+// red: 8 ints.  Called by all 128 threads.
+__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int* red, int& b, int& base) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = p.Hkv * p.rblocks;
+    int before = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < p.B; b0 += kPagedThreads) {
+        const int bi = b0 + threadIdx.x;
+        const int x = bi < p.B ? seq_units(p, bi) * per : 0;
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        int off = before;
+        for (int w = 0; w < warp; ++w) off += red[w];
+        const int all = red[0] + red[1] + red[2] + red[3];
+        incl += off;
+        if (x > 0 && g >= incl - x && g < incl) {
+            red[4] = bi;
+            red[5] = incl - x;
+        }
+        __syncthreads();
+        if (g < before + all) break;
+        before += all;
+    }
+    b = red[4];
+    base = red[5];
+}
+
+// ------------------------------------------------------------------ warp-level pieces
+// 16 (8) bytes from global into shared memory, `bytes` of them read, zeros behind.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// c += A (16 x 16) B (16 x 8), fp32 sums.  HALF: fp16 operands, else bf16.
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two e4m3 values (the low 16 bits of x) as two fp16 values, exactly (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t x) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t x) {
+    float2 y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(y.x), "=f"(y.y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// Copies and products of one 16-key tile of key rows.
+//
+// The product is S^T = K Q^T: 16 keys are the M rows, 8 query rows the N columns.  Lane (g, t)
+// = (lane / 4, lane % 4) of an A fragment holds columns of keys g and g + 8; which columns of d the
+// 16 slots of a k-step stand for is free as long as K and Q agree, so the lane takes 16
+// contiguous bytes of a key row (chunk u: bytes [64u + 16t, +16)) as its slots of 2 (bf16) or 4
+// (e4m3) k-steps.  A lane thus reads back exactly the bytes that it copied: its shared memory is
+// an extension of its registers, without swizzles, barriers or bank conflicts, and the loads
+// in flight are bounded by shared memory alone.
+template <int D, bool F8>
+struct KeyTile {
+    static constexpr int kRow = D * (F8 ? 1 : 2);     // bytes of a row
+    static constexpr int kChunks = kRow / 64;         // 16-byte chunks of a row per lane
+    static constexpr int kElems = F8 ? 16 : 8;        // elements of a chunk
+    static constexpr int kSteps = kElems / 4;         // k-steps of a chunk
+    static constexpr int kBytes = kTileKeys * kRow;   // of a tile
+
+    // rows: the tile's first row; valid: keys of the tile that exist (0..16)
+    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bytes = g + 8 * h < valid ? 16 : 0;
+#pragma unroll
+            for (int u = 0; u < kChunks; ++u)
+                cp_async16(dst + (h * kChunks + u) * 512 + lane * 16, rows + (g + 8 * h) * kRow + u * 64 + t * 16, bytes);
+        }
+    }
+};
+
+// Power of two that brings a query row's largest magnitude into [2^14, 2^15): e4m3 keys meet
+// the query in fp16 (the type that holds e4m3 exactly), and a row scaled so keeps every bf16
+// bit of elements down to 2^-29 of its largest and loses at most 2^-40 of it below.
+// top: largest finite magnitude of the row, 2^(e-127) <= top < 2^(e-126).  The exponent is kept at
+// -110 or more so that both the scale and its inverse are normal numbers.
+__device__ __forceinline__ int query_exponent(float top) {
+    const int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;
+    return top > 0.f ? max(e, -110) : 0;
+}
+
+// 2^e for an exponent byte e + 127 of 1..254.
+__device__ __forceinline__ float exp_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {   // 0 for infinities and NaN
+    const uint32_t x = bf16_bits & 0x7fffu;
+    return x >= 0x7f80u ? 0.f : __uint_as_float(x << 16);
+}
+
+// B fragments of 8 query rows (row0 .. row0 + 7 of the KV head's contiguous rows; rows past `rows`
+// are zeros) for KeyTile<D, F8>: frag[s] of every k-step, and the lane's factor by which a product
+// is turned into a score in base 2 (of row lane / 4).
+template <int D, bool F8>
+__device__ __forceinline__ void load_queries(const uint16_t* q, int row0, int rows, float sl2, uint2* frag, float& factor) {
+    using K = KeyTile<D, F8>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const bool have = row0 + g < rows;
+    const uint16_t* src = q + (size_t)(row0 + g) * D;
+    constexpr int kLoads = D / 32;      // 16-byte loads of a row per lane
+    uint4 v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+        // bf16 keys: chunk u covers columns [32u + 8t, +8); e4m3: [64(u/2) + 16t + 8(u%2), +8)
+        const int col = F8 ? (u >> 1) * 64 + t * 16 + (u & 1) * 8 : u * 32 + t * 8;
+        v[u] = have ? __ldg(reinterpret_cast<const uint4*>(src + col)) : make_uint4(0, 0, 0, 0);
+    }
+    factor = sl2;
+    if (!F8) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            frag[2 * u] = make_uint2(v[u].x, v[u].y);
+            frag[2 * u + 1] = make_uint2(v[u].z, v[u].w);
+        }
+        return;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(finite_abs(w[i]), finite_abs(w[i] >> 16)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = query_exponent(top);
+    const float inv = pow2(-e);
+    factor = pow2(e) * sl2;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = pack_half(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+        frag[2 * u] = make_uint2(h[0], h[1]);
+        frag[2 * u + 1] = make_uint2(h[2], h[3]);
+    }
+}
+
+}  // namespace skl

@@ -1,0 +1,248 @@
+// paged_host.cuh -- host side of the paged-cache entry points: argument checks and launches.
+// Included once, at the end of streamkl.cu.
+#pragma once
+
+namespace {
+
+constexpr int kPagedCtasPerSm = 2;
+
+int page_shift_of(int n) {
+    int s = 0;
+    while ((1 << s) < n) ++s;
+    return s;
+}
+
+// Blocks of 8, 16 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
+int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+int check_cache(const streamkl_cache* c, bool values) {
+    if (!c || !c->k || (values && !c->v)) return STREAMKL_ERR_INVALID_ARG;
+    if (c->type != STREAMKL_CACHE_BF16 && c->type != STREAMKL_CACHE_E4M3) return STREAMKL_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->page_size < 1 || c->Hkv < 1 || c->d < 1) return STREAMKL_ERR_INVALID_ARG;
+    if (c->type == STREAMKL_CACHE_E4M3 && (!c->k_exp || (values && !c->v_exp))) return STREAMKL_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 128) return STREAMKL_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return STREAMKL_ERR_UNSUPPORTED;
+    if (!aligned16(c->k) || !aligned16(c->k_exp) || (values && (!aligned16(c->v) || !aligned16(c->v_exp))))
+        return STREAMKL_ERR_UNSUPPORTED;
+    return STREAMKL_OK;
+}
+
+int check_table(const streamkl_cache* c, const int* table, int width, int B) {
+    if (!table || width < 1 || B < 1) return STREAMKL_ERR_INVALID_ARG;
+    if ((long long)width * c->page_size >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+    return STREAMKL_OK;
+}
+
+int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, const int* table, int width,
+               const int* start, const int* count, int B, int NT, bool append, void* stream) {
+    int rc = check_cache(c, true);
+    if (rc) return rc;
+    if ((rc = check_table(c, table, width, B))) return rc;
+    if (!k || !v || NT < 1) return STREAMKL_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return STREAMKL_ERR_UNSUPPORTED;
+    if ((long long)B * c->Hkv * NT >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+    skl::CacheParams p;
+    p.rows[0] = static_cast<uint8_t*>(c->k);
+    p.rows[1] = static_cast<uint8_t*>(c->v);
+    p.exps[0] = c->k_exp;
+    p.exps[1] = c->v_exp;
+    p.dense[0] = const_cast<uint16_t*>(k);
+    p.dense[1] = const_cast<uint16_t*>(v);
+    p.table = table;
+    p.start = start;
+    p.count = count;
+    p.B = B; p.Hkv = c->Hkv; p.NT = NT; p.width = width; p.pages = c->pages;
+    p.page_size = c->page_size;
+    p.page_shift = page_shift_of(c->page_size);
+    const long long warps = (long long)B * c->Hkv * ((NT + skl::kCacheRows - 1) / skl::kCacheRows);
+    const int per = skl::kCacheThreads / 32;
+    const int grid = (int)std::min<long long>((warps + per - 1) / per, 8ll * num_sms());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool f8 = c->type == STREAMKL_CACHE_E4M3;
+#define SKL_CACHE(D, F8)                                                                          \
+    (append ? skl::streamkl_cache_append_kernel<D, F8><<<grid, skl::kCacheThreads, 0, st>>>(p)    \
+            : skl::streamkl_cache_gather_kernel<D, F8><<<grid, skl::kCacheThreads, 0, st>>>(p))
+    if (c->d == 128) f8 ? SKL_CACHE(128, true) : SKL_CACHE(128, false);
+    else f8 ? SKL_CACHE(64, true) : SKL_CACHE(64, false);
+#undef SKL_CACHE
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, append ? "streamkl_cache_append launch" : "streamkl_cache_gather launch");
+    return STREAMKL_OK;
+}
+
+// Checks and fills what attention and divergence share.
+int paged_params(const streamkl_cache* c, const int* table, int width, const int* lengths, int B, int Hq, int NQ,
+                 float scale, int causal, void* workspace, size_t workspace_bytes, skl::PagedParams* p) {
+    int rc = check_table(c, table, width, B);
+    if (rc) return rc;
+    if (!lengths || Hq < 1 || NQ < 1) return STREAMKL_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return STREAMKL_ERR_UNSUPPORTED;
+    if (Hq % c->Hkv != 0) return STREAMKL_ERR_UNSUPPORTED;
+    if ((long long)B * Hq * NQ >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+    const long long rows = (long long)(Hq / c->Hkv) * NQ;
+    const int nt = paged_row_tiles(rows);
+    const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
+    const long long most = ((long long)width * c->page_size + skl::kUnitKeys - 1) / skl::kUnitKeys;
+    if ((double)B * c->Hkv * (double)rblocks * (double)most >= 2147483648.0) return STREAMKL_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < streamkl_paged_workspace_bytes(B, Hq, c->Hkv, NQ, c->d))
+        return STREAMKL_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return STREAMKL_ERR_UNSUPPORTED;
+    p->table = table;
+    p->lengths = lengths;
+    p->B = B; p->Hkv = c->Hkv; p->NQ = NQ;
+    p->rows = (int)rows;
+    p->rblocks = (int)rblocks;
+    p->width = width;
+    p->pages = c->pages;
+    p->page_size = c->page_size;
+    p->page_shift = page_shift_of(c->page_size);
+    p->causal = causal ? 1 : 0;
+    p->min_units = 1;
+    p->grid = kPagedCtasPerSm * num_sms();
+    p->sl2 = scale * 1.4426950408889634f;
+    p->part = static_cast<float*>(workspace);
+    return STREAMKL_OK;
+}
+
+template <typename K>
+int launch_join(K kernel, const skl::PagedParams& p, int gy, cudaStream_t st, const char* what) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
+    cfg.blockDim = dim3(skl::kPagedThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return STREAMKL_OK;
+}
+
+template <int D, bool F8, int NT>
+int launch_paged_attn(const skl::PagedParams& p, cudaStream_t st) {
+    using C = skl::AttnCfg<D, F8, NT>;
+    auto kern = skl::streamkl_paged_attn_kernel<D, F8, NT>;
+    int rc = set_smem(kern, C::kSmem);
+    if (rc) return rc;
+    kern<<<p.grid, skl::kPagedThreads, C::kSmem, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_attn launch");
+    // few segments: each has many partial states, and its rows go to CTAs of their own
+    const long long segments = (long long)p.B * p.Hkv * p.rblocks;
+    const int gy = segments * 4 <= p.grid ? std::min(p.rows, 8 * NT) : 1;
+    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT>, p, gy, st, "streamkl_paged_attn join launch");
+}
+
+template <int D, bool F8>
+int launch_paged_attn_rows(const skl::PagedParams& p, cudaStream_t st) {
+    switch (paged_row_tiles(p.rows)) {
+        case 1: return launch_paged_attn<D, F8, 1>(p, st);
+        case 2: return launch_paged_attn<D, F8, 2>(p, st);
+        default: return launch_paged_attn<D, F8, 4>(p, st);
+    }
+}
+
+template <int D, bool F1, bool F2, bool SHARED, int NT>
+int launch_paged_kl(const skl::PagedParams& p, cudaStream_t st) {
+    using C = skl::KlCfg<D, F1, F2, SHARED, NT>;
+    auto kern = skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>;
+    int rc = set_smem(kern, C::kSmem);
+    if (rc) return rc;
+    kern<<<p.grid, skl::kPagedThreads, C::kSmem, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_kl launch");
+    return launch_join(skl::streamkl_paged_kl_join_kernel<NT>, p, 1, st, "streamkl_paged_kl join launch");
+}
+
+template <int D, bool F1, bool F2, bool SHARED>
+int launch_paged_kl_rows(const skl::PagedParams& p, cudaStream_t st) {
+    switch (paged_row_tiles(p.rows)) {
+        case 1: return launch_paged_kl<D, F1, F2, SHARED, 1>(p, st);
+        case 2: return launch_paged_kl<D, F1, F2, SHARED, 2>(p, st);
+        default: return launch_paged_kl<D, F1, F2, SHARED, 4>(p, st);
+    }
+}
+
+template <int D>
+int launch_paged_kl_types(const skl::PagedParams& p, bool f1, bool f2, bool shared, cudaStream_t st) {
+    if (shared) return f1 ? launch_paged_kl_rows<D, true, true, true>(p, st) : launch_paged_kl_rows<D, false, false, true>(p, st);
+    if (f1) return f2 ? launch_paged_kl_rows<D, true, true, false>(p, st) : launch_paged_kl_rows<D, true, false, false>(p, st);
+    return f2 ? launch_paged_kl_rows<D, false, true, false>(p, st) : launch_paged_kl_rows<D, false, false, false>(p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int streamkl_cache_append(const streamkl_cache* cache, const uint16_t* k, const uint16_t* v, const int* table,
+                          int width, const int* start, const int* count, int B, int NT, void* stream) {
+    return cache_move(cache, k, v, table, width, start, count, B, NT, true, stream);
+}
+
+int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int width, const int* start,
+                          const int* count, int B, int NT, uint16_t* k, uint16_t* v, void* stream) {
+    return cache_move(cache, k, v, table, width, start, count, B, NT, false, stream);
+}
+
+size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || NQ < 1 || Hq % Hkv || (d != 64 && d != 128)) return 0;
+    const long long rows = (long long)(Hq / Hkv) * NQ;
+    return (size_t)kPagedCtasPerSm * num_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
+}
+
+int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,
+                        const int* lengths, int B, int Hq, int NQ, float scale, int causal, uint16_t* out,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !out || !lse) return STREAMKL_ERR_INVALID_ARG;
+    int rc = check_cache(cache, true);
+    if (rc) return rc;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(lse)) return STREAMKL_ERR_UNSUPPORTED;
+    skl::PagedParams p = {};
+    if ((rc = paged_params(cache, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
+        return rc;
+    p.a = {static_cast<const uint8_t*>(cache->k), cache->k_exp};
+    p.b = {static_cast<const uint8_t*>(cache->v), cache->v_exp};
+    p.q1 = q;
+    p.out = out;
+    p.lse1 = lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool f8 = cache->type == STREAMKL_CACHE_E4M3;
+    if (cache->d == 128) return f8 ? launch_paged_attn_rows<128, true>(p, st) : launch_paged_attn_rows<128, false>(p, st);
+    return f8 ? launch_paged_attn_rows<64, true>(p, st) : launch_paged_attn_rows<64, false>(p, st);
+}
+
+int streamkl_paged_kl(const streamkl_cache* cache1, const uint16_t* q1, const streamkl_cache* cache2,
+                      const uint16_t* q2, const int* table, int width, const int* lengths, int B, int Hq, int NQ,
+                      float scale, int causal, float* kl, float* lse1, float* lse2, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    if (!q1 || !q2 || !kl || !lse1 || !lse2) return STREAMKL_ERR_INVALID_ARG;
+    int rc = check_cache(cache1, false);
+    if (rc) return rc;
+    if ((rc = check_cache(cache2, false))) return rc;
+    if (cache1->pages != cache2->pages || cache1->page_size != cache2->page_size || cache1->Hkv != cache2->Hkv ||
+        cache1->d != cache2->d)
+        return STREAMKL_ERR_UNSUPPORTED;
+    const bool shared = cache1->k == cache2->k;
+    if (shared && (cache1->type != cache2->type || cache1->k_exp != cache2->k_exp)) return STREAMKL_ERR_INVALID_ARG;
+    const void* ptrs[] = {q1, q2, kl, lse1, lse2};
+    for (const void* ptr : ptrs)
+        if (!aligned16(ptr)) return STREAMKL_ERR_UNSUPPORTED;
+    skl::PagedParams p = {};
+    if ((rc = paged_params(cache1, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
+        return rc;
+    p.a = {static_cast<const uint8_t*>(cache1->k), cache1->k_exp};
+    p.b = {static_cast<const uint8_t*>(cache2->k), cache2->k_exp};
+    p.q1 = q1;
+    p.q2 = q2;
+    p.kl = kl;
+    p.lse1 = lse1;
+    p.lse2 = lse2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool f1 = cache1->type == STREAMKL_CACHE_E4M3, f2 = cache2->type == STREAMKL_CACHE_E4M3;
+    return cache1->d == 128 ? launch_paged_kl_types<128>(p, f1, f2, shared, st)
+                            : launch_paged_kl_types<64>(p, f1, f2, shared, st);
+}
+
+}  // extern "C"

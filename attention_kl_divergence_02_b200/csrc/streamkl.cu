@@ -16,6 +16,9 @@
 #include "fwd_kernel.cuh"
 #include "fwd_keys_kernel.cuh"
 #include "bwd_kernel.cuh"
+#include "cache_kernels.cuh"
+#include "paged_attn_kernel.cuh"
+#include "paged_kl_kernel.cuh"
 #include "watchdog.cuh"
 #include "probe.cuh"
 
@@ -197,6 +200,7 @@ const char* streamkl_status_string(int status) {
         case STREAMKL_ERR_UNSUPPORTED: return "unsupported shape, scale or alignment";
         case STREAMKL_ERR_CUDA: return "CUDA error";
         case STREAMKL_ERR_TIMEOUT: return "a kernel pipeline wait timed out";
+        case STREAMKL_ERR_PAGE: return "a page table entry, position or length outside the cache";
         default: return "unknown status";
     }
 }
@@ -213,7 +217,14 @@ int streamkl_device_status(void* stream) {
         e = cudaMemcpyToSymbol(skl::g_status, &zero, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e, "clear device status");
     }
-    return v;
+    int page = 0;
+    e = cudaMemcpyFromSymbol(&page, skl::g_page_status, sizeof(int));
+    if (e != cudaSuccess) return cuda_fail(e, "read device status");
+    if (page != 0) {
+        e = cudaMemcpyToSymbol(skl::g_page_status, &zero, sizeof(int));
+        if (e != cudaSuccess) return cuda_fail(e, "clear device status");
+    }
+    return v != 0 ? v : page;
 }
 
 int streamkl_selftest_watchdog(int starve, long long* waited_ns, void* stream) {
@@ -692,3 +703,5 @@ extern "C" int streamkl_bwd_noalloc(int mode, const uint16_t* q1, const uint16_t
     return streamkl_bwd(mode, q1, k1, q2, k2, kl, lse1, lse2, dkl, B, Hq, Hkv, NQ, NK, d, scale,
                         causal, dq, dk, ws, need, stream);
 }
+
+#include "paged_host.cuh"

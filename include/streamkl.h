@@ -47,7 +47,9 @@ enum {
     STREAMKL_ERR_INVALID_ARG = 1,  /* null pointer, size < 1, mode not 1/2, workspace too small */
     STREAMKL_ERR_UNSUPPORTED = 2,  /* d not 64/128, Hq % Hkv, causal with NQ != NK, alignment */
     STREAMKL_ERR_CUDA = 3,         /* a CUDA runtime or driver call failed (launch, memset) */
-    STREAMKL_ERR_TIMEOUT = 4       /* a kernel gave up on a pipeline wait (device status only) */
+    STREAMKL_ERR_TIMEOUT = 4,      /* a kernel gave up on a pipeline wait (device status only) */
+    STREAMKL_ERR_PAGE = 5          /* a page table entry, position or length outside the cache
+                                      (device status only) */
 };
 
 /*
@@ -206,6 +208,103 @@ int streamkl_bwd_noalloc(int mode, const uint16_t* q1, const uint16_t* k1, const
                          const float* dkl, int B, int Hq, int Hkv, int NQ, int NK, int d,
                          float scale, int causal, uint16_t* dq, uint16_t* dk, void* stream);
 
+/* ------------------------------------------------------------------ paged key-value cache
+ *
+ * Serving form of the same two-distribution setting: keys (and values) of many sequences of
+ * different lengths lie in fixed-size pages, new tokens are written behind them, and a few query
+ * rows per sequence read them (KV cache and grouped heads as in the FlashAttention lecture notes,
+ * hackmd, "3. 架構層級的記憶體妥協").  Lengths, positions and page tables are device data, so every
+ * call below can be captured in a CUDA graph and replayed while they change.
+ *
+ * Conventions of these calls, beyond those at the top:
+ *  - streamkl_cache is a host struct that describes device memory; the library reads it during
+ *    the call only.  One page table row and one length belong to a sequence: token j lies in
+ *    page table[b][j / page_size], slot j % page_size.  int32 tables, lengths, positions and
+ *    counts need 4-byte alignment; every other pointer 16-byte alignment.
+ *  - Several sequences may share pages for reading.  A slot that one append writes twice
+ *    (the same page in two rows of the table) holds a mix of both.
+ *  - Entries of a table row behind the sequence's last page are never used.  A used
+ *    entry outside [0, pages) or a position or length outside [0, width * page_size] is recorded
+ *    (streamkl_device_status returns STREAMKL_ERR_PAGE) and touches no memory: a length is clamped
+ *    to the table, keys of such a page count as masked, such a row is neither written nor read.
+ */
+enum { STREAMKL_CACHE_BF16 = 0, STREAMKL_CACHE_E4M3 = 1 };
+
+typedef struct streamkl_cache {
+    void* k;          /* [pages, Hkv, page_size, d], bf16 or e4m3 */
+    void* v;          /* the same; not used (may be NULL) in streamkl_paged_kl */
+    uint8_t* k_exp;   /* e4m3: [pages, Hkv, page_size], a row's scale is 2^(byte - 127) */
+    uint8_t* v_exp;   /*       (bf16: not used, may be NULL) */
+    int type;         /* STREAMKL_CACHE_* */
+    int pages;
+    int page_size;    /* a power of two, 16 to 1024 */
+    int Hkv;
+    int d;            /* 64 or 128 */
+} streamkl_cache;
+
+/*
+ * Writes token rows into the cache: row i < count[b] of sequence b goes to position start[b] + i.
+ * An e4m3 row gets the scale 2^e, e the least integer >= -96 with max |x| <= 448 * 2^e over its
+ * finite elements, and codes x * 2^-e rounded to nearest even; infinities become the largest
+ * code, NaN stays NaN.  Scales written lie in 2^-96 .. 2^120 (with the last, codes end at 240,
+ * the largest whose value is finite in bf16).
+ *   k, v         : bf16 [B, Hkv, NT, d], the layout of the dense calls.
+ *   table        : int32 [B, width].
+ *   start, count : int32 [B]; NULL: 0 and NT.  A count above NT means NT; below 1, none.
+ * One kernel; lengths are the caller's to advance.
+ */
+int streamkl_cache_append(const streamkl_cache* cache, const uint16_t* k, const uint16_t* v,
+                          const int* table, int width, const int* start, const int* count, int B,
+                          int NT, void* stream);
+
+/*
+ * Reads rows back: row i < count[b] of k and v, bf16 [B, Hkv, NT, d], becomes the cached row at
+ * position start[b] + i (e4m3: code * 2^e, exact in bf16); rows behind the count are left as
+ * they were.  With it the dense calls run over cached keys.  Arguments as streamkl_cache_append.
+ */
+int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int width,
+                          const int* start, const int* count, int B, int NT, uint16_t* k,
+                          uint16_t* v, void* stream);
+
+/*
+ * Bytes of workspace for streamkl_paged_attn and streamkl_paged_kl: two partial states per CTA of a
+ * grid of two per SM of the current device, whatever the lengths are.  Returns 0 for sizes
+ * outside the supported range.
+ */
+size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
+
+/*
+ * Attention of NQ new tokens per sequence over the cache (their own rows appended before).
+ *   out = softmax(scale q K^T) V,   lse = log sum exp(scale q K^T)  (natural log)
+ *   q       : bf16 [B, Hq, NQ, d];  out: bf16, the same shape;  lse: fp32 [B, Hq, NQ].
+ *   lengths : int32 [B], tokens in the cache, the new ones included.
+ *   causal  : nonzero: the NQ tokens are the sequence's last, token i sees keys
+ *             j <= length - NQ + i; zero: every token sees all keys.
+ * A row that sees no key gets zeros and lse = -inf.  What lies in the cache behind a sequence's
+ * length, or behind the last key that a row sees, does not reach the row's result even when it is
+ * not finite.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
+ *   workspace : at least streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d) bytes; contents on entry
+ *               do not matter.  Two calls that run at the same time need two workspaces.
+ * Two kernels; the result does not depend on the order in which CTAs run.
+ */
+int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,
+                        const int* lengths, int B, int Hq, int NQ, float scale, int causal,
+                        uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * The divergence of streamkl_fwd over paged caches, for NQ new tokens per sequence: P1 from q1 and
+ * cache1's keys, P2 from q2 and cache2's, over the same table and lengths.  The caches agree in
+ * everything but type and pointers (a student over a quantised cache against its teacher over the
+ * unquantised one); cache1->k == cache2->k means one cache, whose keys are read once.
+ *   kl, lse1, lse2 : fp32 [B, Hq, NQ].  A row that sees no key: 0, -inf, -inf.
+ * Other arguments as streamkl_paged_attn.
+ */
+int streamkl_paged_kl(const streamkl_cache* cache1, const uint16_t* q1, const streamkl_cache* cache2,
+                      const uint16_t* q2, const int* table, int width, const int* lengths, int B,
+                      int Hq, int NQ, float scale, int causal, float* kl, float* lse1, float* lse2,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Throughput probe of the two exponential paths the kernels use; no part of the KL
  * computation.  The forward spends two exponentials per (row, key) pair with no second GEMM
@@ -264,7 +363,8 @@ const char* streamkl_status_string(int status);
 /*
  * Synchronises `stream`, then reads and clears the device status word of the current
  * device.  Returns STREAMKL_OK, STREAMKL_ERR_TIMEOUT (a kernel abandoned a pipeline wait
- * and left its outputs undefined) or STREAMKL_ERR_CUDA (the synchronisation itself failed;
+ * and left its outputs undefined), STREAMKL_ERR_PAGE (a paged call met a table entry, position or
+ * length outside the cache) or STREAMKL_ERR_CUDA (the synchronisation itself failed;
  * cudaGetLastError text is available through streamkl_last_cuda_error).
  */
 int streamkl_device_status(void* stream);
