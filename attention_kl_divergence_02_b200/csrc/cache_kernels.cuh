@@ -8,9 +8,10 @@
 // mantissa.  2^-96 keeps scale, inverse and every code's value normal in fp32 and bf16.
 // Reading back is exact: 4 significant bits fit bf16.
 //
-// Bound: memory.  Half a warp takes a key row and the other half the same token's value row (16
-// lanes x 8 elements at d = 128), so both share the page lookup; each warp takes 4 tokens of one
-// head at once, whose loads are independent.
+// Bound: memory.  A row takes d / 8 lanes with 16 bytes of bf16 each; of a warp's 2 (d = 128) or 4
+// (d = 64) rows at a time, one half are keys and the other half the same tokens' values, so the pool
+// rows are looked up once for both, by one lane per token, before the loads.  A warp does
+// kCacheTurns such turns, all of whose loads are in flight together.
 #pragma once
 
 #include "paged.cuh"
@@ -18,7 +19,14 @@
 namespace skl {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 4;      // tokens of a warp
+constexpr int kCacheTurns = 8;
+
+template <int D>
+struct CacheCfg {
+    static constexpr int kLanes = D / 8;                  // of a row
+    static constexpr int kGroups = 32 / kLanes;           // rows at a time
+    static constexpr int kTokens = kGroups / 2 * kCacheTurns;   // of a warp
+};
 
 struct CacheParams {
     uint8_t* rows[2];              // key and value pages
@@ -32,25 +40,23 @@ struct CacheParams {
 
 // The pool row of token i of sequence b, head h; -1 where there is nothing to do (behind the count)
 // or nothing that exists (recorded).
-__device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int h, int i) {
-    if (p.count && i >= p.count[b]) return -1;
-    const int s = p.start ? p.start[b] : 0;
-    const long long pos = (long long)s + i;
-    if (s >= 0 && pos < (long long)p.width * p.page_size) {
-        const int page = p.table[(size_t)b * p.width + (pos >> p.page_shift)];
-        if ((unsigned)page < (unsigned)p.pages)
-            return ((long long)page * p.Hkv + h) * p.page_size + (pos & (p.page_size - 1));
+__device__ __forceinline__ int cache_row(const CacheParams& p, int b, int h, int i) {
+    const int n = p.count ? __ldg(p.count + b) : p.NT, s = p.start ? __ldg(p.start + b) : 0;
+    if (i >= n || i >= p.NT) return -1;
+    const unsigned pos = (unsigned)s + (unsigned)i;       // s, i < 2^31: no wrap for s >= 0
+    if (s >= 0 && pos < (unsigned)p.width * (unsigned)p.page_size) {
+        const int page = __ldg(p.table + (size_t)b * p.width + (pos >> p.page_shift));
+        if ((unsigned)page < (unsigned)p.pages) return (page * p.Hkv + h) * p.page_size + (pos & (p.page_size - 1));
     }
     g_page_status = 5;
     return -1;
 }
 
-// The exponent byte of a row whose largest finite magnitude is a.
-__device__ __forceinline__ uint32_t row_exponent(float a) {
-    const uint32_t bits = __float_as_uint(a);
-    // a = f * 2^x; 448 = 1.75 * 2^8.  A subnormal a has x = -127 here, below the floor all the same.
-    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return (uint32_t)(max(e, -96) + 127);
+// The exponent byte of a row whose largest finite magnitude has these bf16 bits: a = f * 2^x,
+// 448 = 1.75 * 2^8.  A subnormal a has exponent field 0, below the floor all the same.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t bits) {
+    const int e = (int)(bits >> 7) - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0);
+    return (uint32_t)max(e, 127 - 96);
 }
 
 // Two fp32 to two e4m3 codes (lo in the low byte), to nearest even, beyond 448 at 448, NaN kept.
@@ -60,127 +66,115 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return y;
 }
 
+// The larger magnitude of two bf16, as bits, infinities and NaN as 0 where FINITE.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t top_bits(uint32_t x) {
+    uint32_t lo = x & 0x7fffu, hi = (x >> 16) & 0x7fffu;
+    if (FINITE) {
+        lo = lo >= 0x7f80u ? 0u : lo;
+        hi = hi >= 0x7f80u ? 0u : hi;
+    }
+    return max(lo, hi);
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_append_kernel(const CacheParams p) {
-    constexpr int kElems = D / 16;                        // of a lane: 8 or 4
-    constexpr int kWords = kElems / 2;
-    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-    const int groups = (p.NT + kCacheRows - 1) / kCacheRows;
-    const long long all = (long long)p.B * p.Hkv * groups;
-    const long long step = (long long)gridDim.x * (kCacheThreads / 32);
-    for (long long w = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5); w < all; w += step) {
-        const int bh = (int)(w / groups), i0 = (int)(w % groups) * kCacheRows;
-        const int b = bh / p.Hkv, h = bh % p.Hkv;
-        long long row[kCacheRows];
-        uint32_t x[kCacheRows][kWords];
+    using C = CacheCfg<D>;
+    const int lane = threadIdx.x & 31, c = lane % C::kLanes, pool = (lane / C::kLanes) & 1, sub = lane / C::kLanes / 2;
+    const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
+    const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+    const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
+    if (bh >= p.B * p.Hkv) return;
+    const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
+    const uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * 8;
+    uint8_t* rows = pool ? p.rows[1] : p.rows[0];
+    int row[kCacheTurns];
+    uint4 x[kCacheTurns];
 #pragma unroll
-        for (int r = 0; r < kCacheRows; ++r) {
-            row[r] = i0 + r < p.NT ? cache_row(p, b, h, i0 + r) : -1;
-            const uint16_t* from = p.dense[half] + ((size_t)bh * p.NT + i0 + r) * D + c * kElems;
+    for (int r = 0; r < kCacheTurns; ++r) {
+        const int i = r * (C::kGroups / 2) + sub;
+        row[r] = __shfl_sync(0xffffffffu, mine, i);
+        x[r] = make_uint4(0, 0, 0, 0);
+        if (row[r] >= 0) x[r] = __ldg(reinterpret_cast<const uint4*>(dense + (size_t)i * D));
+    }
+    if (!F8) {
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) x[r][k] = 0;
-            if (row[r] >= 0) {
-                if (kWords == 4) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(from));
-                    x[r][0] = v.x; x[r][1] = v.y; x[r][kWords - 2] = v.z; x[r][kWords - 1] = v.w;
-                } else {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
-                    x[r][0] = v.x; x[r][1] = v.y;
-                }
-            }
+        for (int r = 0; r < kCacheTurns; ++r)
+            if (row[r] >= 0) *reinterpret_cast<uint4*>(rows + (size_t)row[r] * D * 2 + c * 16) = x[r];
+        return;
+    }
+    uint32_t exponent = 0;                                // lane c < 8 keeps that of turn c
+    int exponent_row = -1;
+#pragma unroll
+    for (int r = 0; r < kCacheTurns; ++r) {
+        uint32_t top = max(max(top_bits<false>(x[r].x), top_bits<false>(x[r].y)), max(top_bits<false>(x[r].z), top_bits<false>(x[r].w)));
+#pragma unroll
+        for (int d = C::kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (__any_sync(0xffffffffu, top >= 0x7f80u)) {
+            top = max(max(top_bits<true>(x[r].x), top_bits<true>(x[r].y)), max(top_bits<true>(x[r].z), top_bits<true>(x[r].w)));
+#pragma unroll
+            for (int d = C::kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         }
+        const uint32_t e = row_exponent(top);
+        const float inv = exp_scale(254u - e);            // 2^-(e - 127)
+        const uint32_t v[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        uint32_t y[4];
 #pragma unroll
-        for (int r = 0; r < kCacheRows; ++r) {
-            if (row[r] < 0) continue;                     // the same in every lane
-            if (!F8) {
-                uint8_t* to = p.rows[half] + (size_t)row[r] * D * 2 + c * kElems * 2;
-                if (kWords == 4)
-                    *reinterpret_cast<uint4*>(to) = make_uint4(x[r][0], x[r][1], x[r][kWords - 2], x[r][kWords - 1]);
-                else
-                    *reinterpret_cast<uint2*>(to) = make_uint2(x[r][0], x[r][1]);
-                continue;
+        for (int k = 0; k < 4; ++k) {
+            float lo = bf16_lo(v[k]) * inv, hi = bf16_hi(v[k]) * inv;
+            if (e == 247) {          // 256 * 2^120 would be infinite: the last scale ends at 240
+                if (fabsf(lo) > 240.f) lo = copysignf(240.f, lo);
+                if (fabsf(hi) > 240.f) hi = copysignf(240.f, hi);
             }
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) top = fmaxf(top, fmaxf(finite_abs(x[r][k]), finite_abs(x[r][k] >> 16)));
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const uint32_t e = row_exponent(top);
-            const float inv = exp_scale(254u - e);        // 2^-(e - 127)
-            uint32_t y[kWords];
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-                float lo = bf16_lo(x[r][k]) * inv, hi = bf16_hi(x[r][k]) * inv;
-                if (e == 247) {          // 256 * 2^120 would be infinite: the last scale ends at 240
-                    if (fabsf(lo) > 240.f) lo = copysignf(240.f, lo);
-                    if (fabsf(hi) > 240.f) hi = copysignf(240.f, hi);
-                }
-                y[k] = e4m3x2(lo, hi);
-            }
-            uint8_t* to = p.rows[half] + (size_t)row[r] * D + c * kElems;
-            if (kWords == 4)
-                *reinterpret_cast<uint2*>(to) = make_uint2(y[0] | y[1] << 16, y[kWords - 2] | y[kWords - 1] << 16);
-            else
-                *reinterpret_cast<uint32_t*>(to) = y[0] | y[1] << 16;
-            if (c == 0) p.exps[half][row[r]] = (uint8_t)e;
+            y[k] = e4m3x2(lo, hi);
+        }
+        if (row[r] >= 0) *reinterpret_cast<uint2*>(rows + (size_t)row[r] * D + c * 8) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+        if (c == r) {
+            exponent = e;
+            exponent_row = row[r];
         }
     }
+    if (exponent_row >= 0) (pool ? p.exps[1] : p.exps[0])[exponent_row] = (uint8_t)exponent;
 }
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_gather_kernel(const CacheParams p) {
-    constexpr int kElems = D / 16;
-    constexpr int kWords = kElems / 2;
-    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-    const int groups = (p.NT + kCacheRows - 1) / kCacheRows;
-    const long long all = (long long)p.B * p.Hkv * groups;
-    const long long step = (long long)gridDim.x * (kCacheThreads / 32);
-    for (long long w = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5); w < all; w += step) {
-        const int bh = (int)(w / groups), i0 = (int)(w % groups) * kCacheRows;
-        const int b = bh / p.Hkv, h = bh % p.Hkv;
-        long long row[kCacheRows];
-        uint32_t x[kCacheRows][kWords], e[kCacheRows];
+    using C = CacheCfg<D>;
+    const int lane = threadIdx.x & 31, c = lane % C::kLanes, pool = (lane / C::kLanes) & 1, sub = lane / C::kLanes / 2;
+    const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
+    const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+    const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
+    if (bh >= p.B * p.Hkv) return;
+    const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
+    uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * 8;
+    const uint8_t* rows = pool ? p.rows[1] : p.rows[0];
+    int row[kCacheTurns];
+    uint4 x[kCacheTurns];
+    uint32_t exponent = 0;
 #pragma unroll
-        for (int r = 0; r < kCacheRows; ++r) {
-            row[r] = i0 + r < p.NT ? cache_row(p, b, h, i0 + r) : -1;
-            if (row[r] < 0) continue;
-            const uint8_t* from = p.rows[half] + (size_t)row[r] * D * (F8 ? 1 : 2) + c * kElems * (F8 ? 1 : 2);
-            if (F8) {
-                e[r] = p.exps[half][row[r]];
-                if (kWords == 4) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(from);
-                    x[r][0] = v.x; x[r][1] = v.y;
-                } else {
-                    x[r][0] = *reinterpret_cast<const uint32_t*>(from);
-                }
-            } else if (kWords == 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(from);
-                x[r][0] = v.x; x[r][1] = v.y; x[r][kWords - 2] = v.z; x[r][kWords - 1] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(from);
-                x[r][0] = v.x; x[r][1] = v.y;
-            }
+    for (int r = 0; r < kCacheTurns; ++r) {
+        row[r] = __shfl_sync(0xffffffffu, mine, r * (C::kGroups / 2) + sub);
+        if (row[r] < 0) continue;
+        if (F8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(rows + (size_t)row[r] * D + c * 8);
+            x[r].x = v.x;
+            x[r].y = v.y;
+            if (c == r) exponent = (pool ? p.exps[1] : p.exps[0])[row[r]];
+        } else {
+            x[r] = *reinterpret_cast<const uint4*>(rows + (size_t)row[r] * D * 2 + c * 16);
         }
+    }
 #pragma unroll
-        for (int r = 0; r < kCacheRows; ++r) {
-            if (row[r] < 0) continue;
-            uint32_t y[kWords];
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-                if (F8) {
-                    const float s = exp_scale(e[r]);
-                    const float2 v = half2_floats(e4m3x2_half2(x[r][k >> 1] >> (16 * (k & 1))));
-                    y[k] = bf16_pair(v.x * s, v.y * s);
-                } else {
-                    y[k] = x[r][k];
-                }
-            }
-            uint16_t* to = p.dense[half] + ((size_t)bh * p.NT + i0 + r) * D + c * kElems;
-            if (kWords == 4)
-                *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[kWords - 2], y[kWords - 1]);
-            else
-                *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+    for (int r = 0; r < kCacheTurns; ++r) {
+        uint4 y = x[r];
+        if (F8) {
+            const float s = exp_scale(__shfl_sync(0xffffffffu, exponent, r, C::kLanes));
+            const float2 v0 = half2_floats(e4m3x2_half2(x[r].x)), v1 = half2_floats(e4m3x2_half2(x[r].x >> 16));
+            const float2 v2 = half2_floats(e4m3x2_half2(x[r].y)), v3 = half2_floats(e4m3x2_half2(x[r].y >> 16));
+            y = make_uint4(bf16_pair(v0.x * s, v0.y * s), bf16_pair(v1.x * s, v1.y * s), bf16_pair(v2.x * s, v2.y * s),
+                           bf16_pair(v3.x * s, v3.y * s));
         }
+        if (row[r] >= 0) *reinterpret_cast<uint4*>(dense + (size_t)(r * (C::kGroups / 2) + sub) * D) = y;
     }
 }
 

@@ -1,13 +1,13 @@
 // paged.cuh -- what the kernels over a paged key-value cache share: the cache's view, the
 // division of the work among a persistent grid, and the warp-level pieces (asynchronous copies
-// into lane-private shared memory, the m16n8k16 product, e4m3 rows).
+// into shared memory, the m16n8k16 product, e4m3 rows).
 //
 // A cache pool holds pages of one kind of row (keys or values), [pages, Hkv, page_size, d],
 // bf16 or e4m3; an e4m3 row has one power-of-two scale, kept as the byte exponent + 127 in
 // [pages, Hkv, page_size].  Sequence b's token j lies in page table[b][j / page_size].
 //
 // Work division.  A segment is one (sequence, KV head, block of query rows); its keys are cut
-// into units of 64.  All segments' units in a row, T of them, are dealt out in equal contiguous
+// into units (of 64 or 128 keys).  All segments' units in a row, T of them, are dealt out in equal contiguous
 // shares of P = ceil(T / grid): lengths are read on the device, so a ragged batch loads every
 // SM alike and the host needs no lengths.  A share may begin or end inside a segment; such a
 // CTA stores a partial state, and a second kernel joins the partial states of a segment in
@@ -26,8 +26,7 @@ __device__ int g_page_status = 0;
 
 constexpr int kPagedThreads = 128;     // 4 warps, each with its own tiles and copies
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr int kTileKeys = 16;          // keys a warp folds at a time (the product's M)
-constexpr int kUnitKeys = kPagedWarps * kTileKeys;
+constexpr int kTileKeys = 16;          // keys of a product (its M)
 constexpr float kNoMax = -3.402823466e38f;   // running maximum before any key
 
 struct PagedPool {
@@ -62,8 +61,10 @@ __device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
+// UNIT: keys of a unit, all warps' tiles once.
+template <int UNIT>
 __device__ __forceinline__ int seq_units(const PagedParams& p, int b) {
-    return (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+    return (seq_len(p, b) + UNIT - 1) / UNIT;
 }
 
 // Sum of x over the CTA's 128 threads, in every thread.  red: 4 ints.
@@ -77,9 +78,10 @@ __device__ __forceinline__ int block_sum(int x, int* red) {
 }
 
 // T: units of all segments.
+template <int UNIT>
 __device__ __forceinline__ int plan_total(const PagedParams& p, int* red) {
     int n = 0;
-    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) n += seq_units(p, b);
+    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) n += seq_units<UNIT>(p, b);
     return block_sum(n, red) * p.Hkv * p.rblocks;
 }
 
@@ -90,6 +92,7 @@ __device__ __forceinline__ int plan_share(const PagedParams& p, int total) {
 
 // The sequence that holds unit g (0 <= g < T), and the first unit of that sequence.
 // red: 8 ints.  Called by all 128 threads.
+template <int UNIT>
 __device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int* red, int& b, int& base) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = p.Hkv * p.rblocks;
@@ -97,7 +100,7 @@ __device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int* re
     __syncthreads();
     for (int b0 = 0; b0 < p.B; b0 += kPagedThreads) {
         const int bi = b0 + threadIdx.x;
-        const int x = bi < p.B ? seq_units(p, bi) * per : 0;
+        const int x = bi < p.B ? seq_units<UNIT>(p, bi) * per : 0;
         int incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -123,12 +126,9 @@ __device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int* re
 }
 
 // ------------------------------------------------------------------ warp-level pieces
-// 16 (8) bytes from global into shared memory, `bytes` of them read, zeros behind.
+// 16 bytes from global into shared memory, `bytes` of them read, zeros behind.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -199,33 +199,61 @@ __device__ __forceinline__ float2 half2_floats(uint32_t x) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Copies and products of one 16-key tile of key rows.
+// A 16-row tile of keys or values in shared memory.  A warp copies its own tiles with coalesced
+// 16-byte copies (consecutive lanes, consecutive chunks: the tile is contiguous in its page) and
+// reads them back as fragments; `place` is where a row's 16-byte chunk lies, such that both the copies
+// and the fragment loads touch every bank once.  (Copying straight into fragment order instead,
+// lane by lane, costs the value tiles four sectors of four different lines per quarter-warp:
+// 219 against 168 us for 131072 keys of 16 heads.)
 //
-// The product is S^T = K Q^T: 16 keys are the M rows, 8 query rows the N columns.  Lane (g, t)
+// Keys: the product is S^T = K Q^T: 16 keys are the M rows, 8 query rows the N columns.  Lane (g, t)
 // = (lane / 4, lane % 4) of an A fragment holds columns of keys g and g + 8; which columns of d the
 // 16 slots of a k-step stand for is free as long as K and Q agree, so the lane takes 16
 // contiguous bytes of a key row (chunk u: bytes [64u + 16t, +16)) as its slots of 2 (bf16) or 4
-// (e4m3) k-steps.  A lane thus reads back exactly the bytes that it copied: its shared memory is
-// an extension of its registers, without swizzles, barriers or bank conflicts, and the loads
-// in flight are bounded by shared memory alone.
+// (e4m3) k-steps.  The 8 lanes of a load phase meet chunks t of two neighbouring rows.
 template <int D, bool F8>
-struct KeyTile {
+struct RowTile {
     static constexpr int kRow = D * (F8 ? 1 : 2);     // bytes of a row
-    static constexpr int kChunks = kRow / 64;         // 16-byte chunks of a row per lane
+    static constexpr int kRowChunks = kRow / 16;
+    static constexpr int kBytes = kTileKeys * kRow;   // of a tile
+    static constexpr int kCopies = kBytes / 512;      // of a lane
+
+    // rows: the tile's first row; valid: rows of the tile that exist (none: at most 0; zeros behind them)
+    template <typename Place>
+    __device__ static __forceinline__ void copy_by(uint32_t dst, const uint8_t* rows, int valid, int lane, Place place) {
+        const uint8_t* from = rows + lane * 16;
+        if (valid >= kTileKeys) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int at = i * 32 + lane;
+                cp_async16(dst + place(at / kRowChunks, at % kRowChunks), from + i * 512, 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int at = i * 32 + lane;
+                cp_async16(dst + place(at / kRowChunks, at % kRowChunks), from + i * 512, at / kRowChunks < valid ? 16 : 0);
+            }
+        }
+    }
+};
+
+template <int D, bool F8>
+struct KeyTile : RowTile<D, F8> {
+    using R = RowTile<D, F8>;
+    static constexpr int kChunks = R::kRow / 64;      // 16-byte chunks of a row per lane
     static constexpr int kElems = F8 ? 16 : 8;        // elements of a chunk
     static constexpr int kSteps = kElems / 4;         // k-steps of a chunk
-    static constexpr int kBytes = kTileKeys * kRow;   // of a tile
 
-    // rows: the tile's first row; valid: keys of the tile that exist (0..16)
+    __device__ static __forceinline__ int place(int row, int chunk) {
+        return row * R::kRow + ((R::kRow >= 128 ? chunk ^ ((row & 1) * 4) : chunk) * 16);
+    }
     __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int bytes = g + 8 * h < valid ? 16 : 0;
-#pragma unroll
-            for (int u = 0; u < kChunks; ++u)
-                cp_async16(dst + (h * kChunks + u) * 512 + lane * 16, rows + (g + 8 * h) * kRow + u * 64 + t * 16, bytes);
-        }
+        R::copy_by(dst, rows, valid, lane, place);
+    }
+    // chunk u of key g + 8h
+    __device__ static __forceinline__ uint4 load(uint32_t src, int h, int u, int lane) {
+        return lds128(src + place((lane >> 2) + 8 * h, (lane & 3) + 4 * u));
     }
 };
 
@@ -285,7 +313,7 @@ __device__ __forceinline__ void load_queries(const uint16_t* q, int row0, int ro
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = query_exponent(top);
     const float inv = pow2(-e);
-    factor = pow2(e) * sl2;
+    factor = fmaxf(pow2(e) * sl2, 1.17549435e-38f);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};

@@ -7,14 +7,14 @@
 //
 // Bound: every cached byte is read once and used for 2 flops per query row and element, so with the
 // few rows of a KV head (Hq / Hkv * NQ) the floor is cache bytes / HBM bandwidth.  Everything here
-// serves the loads: each warp streams its own 16-key tiles through a ring of cp.async stages that
-// only it touches (see KeyTile), so no barrier stands between a load and the next.
+// serves the loads: each warp streams its own tiles through a ring of cp.async slots that only it
+// touches (see RowTile), so no barrier of the CTA stands between a load and the next.
 //
 // Per tile a warp computes S^T = K Q^T (16 keys x 8 rows per product), takes the maxima over the
 // lanes that share a row, and turns P^T around with movmatrix into the B operand of
 // O^T = V^T P^T (M: 16 columns of d, N: 8 rows, K: 16 keys).  V^T's fragments need two keys'
-// values of one column in a register: the lane copies the same 16 bytes of four keys and joins
-// them with byte permutes.
+// values of one column in a register: the lane loads the same bytes of four keys and joins them with
+// byte permutes.
 //
 // bf16 cache: P is split into two bf16 terms (hi + lo, 16 bits of it), because one bf16 rounding of P
 // (up to 2^-9 of each weight) would add as much error as the output's own rounding; the tensor pipe
@@ -29,55 +29,61 @@
 
 namespace skl {
 
+// Values: lane (g, t) of V^T's fragments holds columns of keys 2t, 2t + 1, 2t + 8 and 2t + 9, and takes
+// kElems contiguous ones of each: chunk g (and g + 8 where a row has 16), or half a chunk where it has
+// four.  The lanes of a load phase meet rows 2t of all t.
 template <int D, bool F8>
-struct ValueTile {
-    static constexpr int kRow = D * (F8 ? 1 : 2);
-    static constexpr int kLane = kRow / 8;                      // bytes of a row per lane
-    static constexpr int kCopy = kLane < 16 ? kLane : 16;       // bytes of one copy
-    static constexpr int kChunks = kLane / kCopy;
-    static constexpr int kElems = kCopy / (F8 ? 1 : 2);         // elements of a copy
-    static constexpr int kBytes = kTileKeys * kRow;
+struct ValueTile : RowTile<D, F8> {
+    using R = RowTile<D, F8>;
+    static constexpr int kLane = R::kRow / 8;                   // bytes of a row per lane
+    static constexpr int kLoad = kLane < 16 ? kLane : 16;       // bytes of one load
+    static constexpr int kChunks = kLane / kLoad;
+    static constexpr int kElems = kLoad / (F8 ? 1 : 2);         // elements of a load
 
-    // lane (g, t): chunk g (and g + 8 where a row has 16) of keys 2t, 2t+1, 2t+8, 2t+9
     __device__ static __forceinline__ int key(int j, int t) { return 2 * t + (j & 1) + 8 * (j >> 1); }
 
-    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = key(j, t) < valid;
-#pragma unroll
-            for (int u = 0; u < kChunks; ++u) {
-                const uint32_t to = dst + (j * kChunks + u) * 32 * kCopy + lane * kCopy;
-                const uint8_t* from = rows + key(j, t) * kRow + (u * 8 + g) * kCopy;
-                if (kCopy == 16) cp_async16(to, from, in ? 16 : 0);
-                else cp_async8(to, from, in ? 8 : 0);
-            }
-        }
+    __device__ static __forceinline__ int place(int row, int chunk) {
+        if (R::kRow >= 128) return row * R::kRow + (chunk ^ (row & 6)) * 16;
+        return ((row & 1) + (row >> 2) * 2) * 128 + ((row >> 1) & 1) * 64 + (chunk ^ (((row >> 2) & 1) * 2)) * 16;
     }
-    // the lane's words (4 bytes) of key j, chunk u
+    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
+        R::copy_by(dst, rows, valid, lane, place);
+    }
+    // the lane's words (4 bytes) of key j, load u
     __device__ static __forceinline__ void load(uint32_t src, int j, int u, int lane, uint32_t* w) {
-        const uint32_t from = src + (j * kChunks + u) * 32 * kCopy + lane * kCopy;
-        if (kCopy == 16) {
-            const uint4 v = lds128(from);
+        const int row = key(j, lane & 3), g = lane >> 2;
+        if (kLoad == 16) {
+            const uint4 v = lds128(src + place(row, g + 8 * u));
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         } else {
-            const uint2 v = lds64(from);
+            const uint2 v = lds64(src + place(row, g >> 1) + (g & 1) * 8);
             w[0] = v.x; w[1] = v.y;
         }
     }
 };
 
+// NT: blocks of 8 query rows; a warp folds H 16-key tiles at a time.  Two tiles halve the shuffles,
+// rescalings and waits per key and give the products two independent chains; for more than 16 rows the
+// registers do not hold them.
 template <int D, bool F8, int NT>
 struct AttnCfg {
     using K = KeyTile<D, F8>;
     using V = ValueTile<D, F8>;
+    static constexpr int H = NT > 2 || (D == 128 && (!F8 || NT == 2)) ? 1 : 2;
+    static constexpr int kCtas = NT == 1 ? 3 : 2;                      // on an SM
+    static constexpr int kKeys = H * kTileKeys;                        // of a warp at a time
+    static constexpr int kUnit = kPagedWarps * kKeys;
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
-    static constexpr int kExps = F8 ? 32 : 0;                          // 16 key, 16 value exponents
-    static constexpr int kStage = K::kBytes + V::kBytes + kExps;
-    static constexpr int kStages = (D == 128 && !F8) ? 3 : (D == 64 && F8) ? 8 : 6;
-    static constexpr int kWarp = kStage * kStages;
+    // A slot holds the keys or the values of kKeys tokens, and their exponents.  The slots form a ring,
+    // keys and values in turn; their number is odd, so that the slot refilled after a key (value) slot
+    // is used again takes keys (values).
+    static constexpr int kExps = H * K::kBytes;
+    static constexpr int kSlot = H * K::kBytes + (F8 ? kKeys : 0);
+    static constexpr int kFit = (kCtas == 3 ? 17 : 26) * 1024 / kSlot;   // a warp's share of shared memory
+    static constexpr int kSlots = kFit >= 9 ? 9 : (kFit % 2 ? kFit : kFit - 1);
+    static constexpr int kAhead = (kSlots - 1) / 2;                    // tiles in flight
+    static constexpr int kWarp = kSlot * kSlots;
     static constexpr int kStride = D + 4;                              // floats of a row's state
     static constexpr bool kSharedQ = NT > 2;                           // query fragments in shared memory
     static constexpr int kQ = kPagedWarps * kWarp;
@@ -86,7 +92,10 @@ struct AttnCfg {
     static constexpr int kRed = kStats + kPagedWarps * 3 * kRows * 4;
     static constexpr int kSmem = kRed + 64;
     static constexpr int kPart = kRows * kStride;                      // floats of a partial state
-    static_assert(kWarp >= kRows * kStride * 4, "a warp's state is joined in its stages");
+    static_assert(kSlots >= 3 && kSlots % 2 == 1, "ring");
+    static_assert(kWarp >= kRows * kStride * 4, "a warp's state is joined in its slots");
+    static_assert(K::kBytes == V::kBytes, "one slot size");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "resident CTAs");
 };
 
 // Four columns of a finished row: o / l, rounded once to bf16, and the row's lse.  Weights that refer to
@@ -104,17 +113,17 @@ __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, in
 }
 
 template <int D, bool F8, int NT>
-__global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) streamkl_paged_attn_kernel(const PagedParams p) {
     using C = AttnCfg<D, F8, NT>;
     using K = typename C::K;
     using V = typename C::V;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
-    const uint32_t stage0 = sb + warp * C::kWarp;
+    const uint32_t ring = sb + warp * C::kWarp;
+    constexpr int H = C::H;
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
     int* red = reinterpret_cast<int*>(smem + C::kRed);
-    const int head_stride = p.page_size * K::kRow;       // bytes of one page of one head
 
     // sequences without keys: zeros and -inf
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -126,49 +135,70 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
         for (size_t i = threadIdx.x; i < n; i += kPagedThreads) p.lse1[r0 + i] = -INFINITY;
     }
 
-    const int total = plan_total(p, red);
+    const int total = plan_total<C::kUnit>(p, red);
     const int share = plan_share(p, total);
     const long long first = (long long)blockIdx.x * share;
     if (first >= total) return;
     const int g0 = (int)first, g1 = (int)min((long long)total, first + share);
     int b, base;
-    plan_locate(p, g0, red, b, base);
-    int len = seq_len(p, b), units = (len + kUnitKeys - 1) / kUnitKeys;
+    plan_locate<C::kUnit>(p, g0, red, b, base);
+    int len = seq_len(p, b), units = (len + C::kUnit - 1) / C::kUnit;
 
     for (int pos = g0; pos < g1;) {
         const int off = pos - base, seg = off / units, u0 = off - seg * units;
-        const int n = min(units - u0, g1 - pos);          // units, hence tiles of a warp
+        const int n = min(units - u0, g1 - pos);          // units, hence turns of a warp
         const int h = seg / p.rblocks, rb = seg - h * p.rblocks;
         const int row0 = rb * C::kRows;
         const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)b * p.width;
-        const int key00 = u0 * kUnitKeys + warp * kTileKeys;
-        uint32_t bad = 0;                                 // stages whose page does not exist
+        const int key00 = u0 * C::kUnit + warp * C::kKeys;
 
-        auto issue = [&](int i, int s) {
-            const int key0 = key00 + i * kUnitKeys;
-            const uint32_t dst = stage0 + s * C::kStage;
-            bad &= ~(1u << s);
-            if (key0 < len) {
-                const int page = __ldg(table + (key0 >> p.page_shift));
-                if ((unsigned)page < (unsigned)p.pages) {
-                    const size_t row = ((size_t)page * p.Hkv + h) * p.page_size + (key0 & (p.page_size - 1));
-                    const int valid = len - key0;
-                    K::copy(dst, p.a.rows + row * K::kRow, valid, lane);
-                    V::copy(dst + K::kBytes, p.b.rows + row * V::kRow, valid, lane);
-                    if (F8 && lane < 2)
-                        cp_async16(dst + K::kBytes + V::kBytes + lane * 16, (lane ? p.b.exps : p.a.exps) + row, 16);
-                } else {
-                    bad |= 1u << s;
-                    if (lane == 0) g_page_status = 5;
+        // The turn whose rows are requested next: its pages (looked up one turn before), pool rows and
+        // number of existing keys of each tile.
+        int page[H], row[H], valid[H];
+        uint32_t bad = 0;                                 // bit (turn % 16) * 2 + tile: no such page
+        auto look_up = [&](int i) {
+#pragma unroll
+            for (int x = 0; x < H; ++x) {
+                const int key = key00 + i * C::kUnit + x * kTileKeys;
+                page[x] = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
+            }
+        };
+        auto request_keys = [&](int i, uint32_t dst) {
+            if (i < n) {
+                bad &= ~(3u << ((i & 15) * 2));
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    const int key = key00 + i * C::kUnit + x * kTileKeys;
+                    const bool there = (unsigned)page[x] < (unsigned)p.pages;
+                    valid[x] = there ? len - key : 0;
+                    row[x] = there && key < len ? (page[x] * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
+                    if (!there) {
+                        bad |= 1u << ((i & 15) * 2 + x);
+                        if (lane == 0) g_page_status = 5;
+                    }
+                    K::copy(dst + x * K::kBytes, p.a.rows + (size_t)row[x] * K::kRow, valid[x], lane);
+                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.a.exps + row[x], 16);
+                }
+                look_up(i + 1);
+            }
+            cp_commit();
+        };
+        auto request_values = [&](int i, uint32_t dst) {
+            if (i < n) {
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    V::copy(dst + x * V::kBytes, p.b.rows + (size_t)row[x] * V::kRow, valid[x], lane);
+                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.b.exps + row[x], 16);
                 }
             }
             cp_commit();
         };
+        look_up(0);
 #pragma unroll
-        for (int s = 0; s < C::kStages - 1; ++s) {
-            if (s < n) issue(s, s);
-            else cp_commit();
+        for (int i = 0; i < C::kAhead; ++i) {
+            request_keys(i, ring + 2 * i * C::kSlot);
+            request_values(i, ring + (2 * i + 1) * C::kSlot);
         }
 
         // queries of this segment, as B fragments
@@ -199,16 +229,14 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
                 fac[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }
         }
-        // first key that a row does not see; the least over all rows
-        int lim[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                lim[nt][j] = p.causal ? len - (p.NQ - 1) + (row0 + nt * 8 + 2 * t + j) % p.NQ : len;
+        // first key that a row does not see (of query 2t + j of block nt); the least over all rows
+        auto limit = [&](int nt, int j) {
+            return p.causal ? len - (p.NQ - 1) + (row0 + nt * 8 + 2 * t + j) % p.NQ : len;
+        };
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        float o[D / 16][NT][4], m[NT][2], mv[NT][2], l[NT][2];
+        // m: running maximum of the scores; r: reference of the weights (bf16: m); l: sum
+        float o[D / 16][NT][4], m[NT][2], r[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -219,209 +247,294 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[nt][j] = mv[nt][j] = kNoMax;
+                m[nt][j] = r[nt][j] = kNoMax;
                 l[nt][j] = 0.f;
             }
+        bool tame = true;       // e4m3: every value scale so far within 2^-40 .. 2^40
 
-        int st = 0;
-        for (int i = 0; i < n; ++i, st = st + 1 == C::kStages ? 0 : st + 1) {
-            __syncwarp();       // every lane is done with the stage that is filled next
-            if (i + C::kStages - 1 < n) issue(i + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
-            else cp_commit();
-            cp_wait<C::kStages - 1>();
-            __syncwarp();       // the exponents were copied by lanes 0 and 1
-            const int key0 = key00 + i * kUnitKeys;
-            if (key0 >= len || ((bad >> st) & 1u)) continue;
-            const uint32_t ks = stage0 + st * C::kStage, vs = ks + K::kBytes, es = vs + V::kBytes;
-
-            // S^T
-            float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-            for (int u = 0; u < K::kChunks; ++u) {
-                const uint4 x = lds128(ks + u * 512 + lane * 16), y = lds128(ks + (K::kChunks + u) * 512 + lane * 16);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int w = 0; w < K::kSteps; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    if (F8) {
-                        a0 = e4m3x2_half2(xw[w]);
-                        a1 = e4m3x2_half2(yw[w]);
-                        a2 = e4m3x2_half2(xw[w] >> 16);
-                        a3 = e4m3x2_half2(yw[w] >> 16);
-                    } else {
-                        a0 = xw[(2 * w) & 3];
-                        a1 = yw[(2 * w) & 3];
-                        a2 = xw[(2 * w + 1) & 3];
-                        a3 = yw[(2 * w + 1) & 3];
-                    }
-                    const int step = u * K::kSteps + w;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint2 q = C::kSharedQ ? lds64(sb + C::kQ + ((nt * C::kSteps + step) * 32 + lane) * 8)
-                                                    : qf[C::kSharedQ ? 0 : nt * C::kSteps + step];
-                        mma16816<F8>(s[nt], a0, a1, a2, a3, q.x, q.y);
-                    }
-                }
-            }
-            // scores in base 2; ev: exponents of the values' scales
-            float ev[2] = {0.f, 0.f};
-            if (F8) {
-                const float k0 = exp_scale(lds8(es + g)), k1 = exp_scale(lds8(es + 8 + g));
-                ev[0] = (float)((int)lds8(es + 16 + g) - 127);
-                ev[1] = (float)((int)lds8(es + 24 + g) - 127);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    s[nt][0] = s[nt][0] * fac[nt][0] * k0;
-                    s[nt][1] = s[nt][1] * fac[nt][1] * k0;
-                    s[nt][2] = s[nt][2] * fac[nt][0] * k1;
-                    s[nt][3] = s[nt][3] * fac[nt][1] * k1;
-                }
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[nt][c] *= fac[nt][c & 1];
-            }
-            const bool edge = key0 + kTileKeys > least;
-            if (edge) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (key0 + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[nt][c] = -INFINITY;
-            }
-            // maxima over the tile's keys (the 8 lanes with this t), rescaling, weights
-            uint32_t ph[NT][2], pl[NT][2];      // B fragments of P^T: hi and lo (bf16), or P' (fp16)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(s[nt][j], s[nt][j + 2]);
-                    float topv = F8 ? fmaxf(s[nt][j] + ev[0], s[nt][j + 2] + ev[1]) : 0.f;
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (F8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-                    }
-                    const float mn = fmaxf(m[nt][j], top);
-                    const float a = ex2(m[nt][j] - mn);
-                    m[nt][j] = mn;
-                    const float p0 = ex2(s[nt][j] - mn), p1 = ex2(s[nt][j + 2] - mn);
-                    l[nt][j] = fmaf(l[nt][j], a, p0 + p1);
-                    float av = a;
-                    if (F8) {
-                        const float vn = fmaxf(mv[nt][j], topv);
-                        av = ex2(mv[nt][j] - vn);
-                        mv[nt][j] = vn;
-                        w[j] = ex2(s[nt][j] + ev[0] - vn);
-                        w[j + 2] = ex2(s[nt][j + 2] + ev[1] - vn);
-                    } else {
-                        w[j] = p0;
-                        w[j + 2] = p1;
-                    }
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        o[k][nt][j] *= av;
-                        o[k][nt][j + 2] *= av;
-                    }
-                }
-                if (F8) {
-                    ph[nt][0] = movmatrix(pack_half(w[0], w[1]));
-                    ph[nt][1] = movmatrix(pack_half(w[2], w[3]));
-                } else {
-                    const uint32_t h0 = bf16_pair(w[0], w[1]), h1 = bf16_pair(w[2], w[3]);
-                    ph[nt][0] = movmatrix(h0);
-                    ph[nt][1] = movmatrix(h1);
-                    pl[nt][0] = movmatrix(bf16_pair(w[0] - bf16_lo(h0), w[1] - bf16_hi(h0)));
-                    pl[nt][1] = movmatrix(bf16_pair(w[2] - bf16_lo(h1), w[3] - bf16_hi(h1)));
-                }
-            }
-            // O^T += V^T P^T
-            uint32_t v[V::kChunks][4][4];
-#pragma unroll
-            for (int u = 0; u < V::kChunks; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) V::load(vs, j, u, lane, v[u][j]);
-            // A row that does not see a key must not meet its values even with weight 0 (0 * inf and
-            // 0 * NaN are NaN): where such a tile holds values that are not finite, each query
-            // position is done by itself with the keys behind its limit cleared.
-            bool slow = false;
-            if (edge && least < len) {
-                bool odd = false;
-#pragma unroll
-                for (int u = 0; u < V::kChunks; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int w = 0; w < V::kCopy / 4; ++w)
-#pragma unroll
-                            for (int e = 0; e < 32; e += F8 ? 8 : 16)
-                                odd |= F8 ? ((v[u][j][w] >> e) & 0x7fu) == 0x7fu
-                                          : ((v[u][j][w] >> e) & 0x7f80u) == 0x7f80u;
-                slow = __any_sync(0xffffffffu, odd);
-            }
-            auto fragment = [&](int mt, uint32_t* a, const uint32_t* mask) {
-                // m-tile mt: columns 2x, 2x + 1 of the lane's elements of chunk u
-                const int u = mt / (V::kElems / 2), x = mt % (V::kElems / 2);
-                const int w = F8 ? x >> 1 : x;
-                const uint32_t k0 = v[u][0][w] & mask[0], k1 = v[u][1][w] & mask[1];
-                const uint32_t k2 = v[u][2][w] & mask[2], k3 = v[u][3][w] & mask[3];
-                if (F8) {
-                    const uint32_t sel = (x & 1) ? 0x7362u : 0x5140u;
-                    const uint32_t lo = __byte_perm(k0, k1, sel), hi = __byte_perm(k2, k3, sel);
-                    a[0] = e4m3x2_half2(lo);
-                    a[1] = e4m3x2_half2(lo >> 16);
-                    a[2] = e4m3x2_half2(hi);
-                    a[3] = e4m3x2_half2(hi >> 16);
-                } else {
-                    a[0] = __byte_perm(k0, k1, 0x5410);
-                    a[1] = __byte_perm(k0, k1, 0x7632);
-                    a[2] = __byte_perm(k2, k3, 0x5410);
-                    a[3] = __byte_perm(k2, k3, 0x7632);
-                }
-            };
-            if (!slow) {
-                const uint32_t all[4] = {~0u, ~0u, ~0u, ~0u};
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    uint32_t a[4];
-                    fragment(mt, a, all);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816<F8>(o[mt][nt], a[0], a[1], a[2], a[3], ph[nt][0], ph[nt][1]);
-                        if (!F8) mma16816<F8>(o[mt][nt], a[0], a[1], a[2], a[3], pl[nt][0], pl[nt][1]);
-                    }
-                }
-            } else {
+        uint32_t cur = ring, last = ring + (C::kSlots - 1) * C::kSlot;   // slots of this item and the one before
+        auto advance = [&]() {
+            last = cur;
+            cur = cur == ring + (C::kSlots - 1) * C::kSlot ? ring : cur + C::kSlot;
+        };
 #pragma unroll 1
-                for (int i0 = 0; i0 < p.NQ; ++i0) {
-                    uint32_t mask[4];
+        for (int i = 0; i < n; ++i) {
+            const int key0 = key00 + i * C::kUnit;
+            __syncwarp();       // every lane is done with the slot that is refilled
+            request_keys(i + C::kAhead, last);
+            cp_wait<C::kSlots - 1>();
+            __syncwarp();       // the exponents were copied by single lanes
+            const bool some = key0 < len;
+            const bool edge = key0 + C::kKeys > least || ((bad >> ((i & 15) * 2)) & 3u);
+            auto seen = [&](int x, int k, int nt, int j) {     // key g + 8k of tile x, query 2t + j of block nt
+                return key0 + x * kTileKeys + g + 8 * k < limit(nt, j) && !((bad >> ((i & 15) * 2 + x)) & 1u);
+            };
+
+            // S^T, not yet scaled by fac
+            float s[H][NT][4];
+            if (some) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mask[j] = key0 + V::key(j, t) < least + i0 ? ~0u : 0u;
+                for (int x = 0; x < H; ++x)
 #pragma unroll
-                    for (int mt = 0; mt < D / 16; ++mt) {
-                        uint32_t a[4];
-                        fragment(mt, a, mask);
+                    for (int nt = 0; nt < NT; ++nt) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
+#pragma unroll
+                for (int u = 0; u < K::kChunks; ++u)
+#pragma unroll
+                    for (int x = 0; x < H; ++x) {
+                        const uint4 y0 = K::load(cur + x * K::kBytes, 0, u, lane), y1 = K::load(cur + x * K::kBytes, 1, u, lane);
+                        const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                        for (int w = 0; w < K::kSteps; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            if (F8) {
+                                a0 = e4m3x2_half2(w0[w]);
+                                a1 = e4m3x2_half2(w1[w]);
+                                a2 = e4m3x2_half2(w0[w] >> 16);
+                                a3 = e4m3x2_half2(w1[w] >> 16);
+                            } else {
+                                a0 = w0[(2 * w) & 3];
+                                a1 = w1[(2 * w) & 3];
+                                a2 = w0[(2 * w + 1) & 3];
+                                a3 = w1[(2 * w + 1) & 3];
+                            }
+                            const int step = u * K::kSteps + w;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint2 q = C::kSharedQ ? lds64(sb + C::kQ + ((nt * C::kSteps + step) * 32 + lane) * 8)
+                                                            : qf[C::kSharedQ ? 0 : nt * C::kSteps + step];
+                                mma16816<F8>(s[x][nt], a0, a1, a2, a3, q.x, q.y);
+                            }
+                        }
+                    }
+                if (F8) {
+#pragma unroll
+                    for (int x = 0; x < H; ++x) {
+                        const float k0 = exp_scale(lds8(cur + C::kExps + x * 16 + g)), k1 = exp_scale(lds8(cur + C::kExps + x * 16 + 8 + g));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float c[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816<F8>(c, a[0], a[1], a[2], a[3], ph[nt][0], ph[nt][1]);
-                            if (!F8) mma16816<F8>(c, a[0], a[1], a[2], a[3], pl[nt][0], pl[nt][1]);
+                            s[x][nt][0] *= k0;
+                            s[x][nt][1] *= k0;
+                            s[x][nt][2] *= k1;
+                            s[x][nt][3] *= k1;
+                        }
+                    }
+                }
+                if (edge) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (lim[nt][k & 1] == least + i0) o[mt][nt][k] += c[k];
+                    for (int x = 0; x < H; ++x)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (!seen(x, c >> 1, nt, c & 1)) s[x][nt][c] = -INFINITY;
+                }
+            }
+            advance();
+
+            __syncwarp();
+            request_values(i + C::kAhead, last);
+            cp_wait<C::kSlots - 1>();
+            __syncwarp();
+            if (some) {
+                // e4m3: scales of the values, their exponents' range over the turn's keys
+                float kv[H][2];
+                int e_max = 0;
+                bool near = true;
+                if (F8) {
+                    uint32_t e = lds8(cur + C::kExps + (lane & (C::kKeys - 1)));
+                    const bool in = !edge || (key0 + (lane & (C::kKeys - 1)) < len &&
+                                              !((bad >> ((i & 15) * 2 + ((lane & (C::kKeys - 1)) >> 4))) & 1u));
+                    e_max = (int)__reduce_max_sync(0xffffffffu, in ? e : 0u);
+                    const int e_min = (int)__reduce_min_sync(0xffffffffu, in ? e : 255u);
+                    tame = tame && e_min >= 127 - 40 && e_max <= 127 + 40;
+                    near = tame && e_max - e_min <= 8;
+                    e_max -= 127;
+#pragma unroll
+                    for (int x = 0; x < H; ++x)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t b8 = lds8(cur + C::kExps + x * 16 + 8 * k + g);
+                            if (edge && !(key0 + x * 16 + 8 * k + g < len && !((bad >> ((i & 15) * 2 + x)) & 1u))) b8 = 127;
+                            kv[x][k] = near ? exp_scale(b8) : (float)((int)b8 - 127);
+                        }
+                }
+                // maxima over the turn's keys (the 8 lanes with this t), rescaling, weights
+                float mn[NT][2], rn[NT][2];
+                bool grew = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float top = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+                        if (H == 2) top = fmaxf(top, fmaxf(s[H - 1][nt][j], s[H - 1][nt][j + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        top *= fac[nt][j];
+                        mn[nt][j] = fmaxf(m[nt][j], top);
+                        if (F8) {
+                            float ref = top + (float)e_max;
+                            if (!near) {
+                                ref = kNoMax;
+#pragma unroll
+                                for (int x = 0; x < H; ++x)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) ref = fmaxf(ref, fmaf(s[x][nt][j + 2 * k], fac[nt][j], kv[x][k]));
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+                            }
+                            rn[nt][j] = fmaxf(r[nt][j], ref);
+                            grew |= rn[nt][j] > r[nt][j];
+                        }
+                        grew |= mn[nt][j] > m[nt][j];
+                    }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float a = ex2(m[nt][j] - mn[nt][j]);
+                            l[nt][j] *= a;
+                            m[nt][j] = mn[nt][j];
+                            float av = a;
+                            if (F8) {
+                                av = ex2(r[nt][j] - rn[nt][j]);
+                                r[nt][j] = rn[nt][j];
+                            }
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                o[k][nt][j] *= av;
+                                o[k][nt][j + 2] *= av;
+                            }
+                        }
+                }
+                uint32_t ph[H][NT][2], pl[H][NT][2];    // B fragments of P^T: hi and lo (bf16), or P' (fp16)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[H][4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float f = F8 && near ? ex2(m[nt][j] - r[nt][j]) : 1.f;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int x = 0; x < H; ++x)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float q = ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], -m[nt][j]));
+                                sum += q;
+                                w[x][j + 2 * k] = !F8 ? q
+                                                : near ? q * (f * kv[x][k])
+                                                       : ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], kv[x][k]) - r[nt][j]);
+                            }
+                        l[nt][j] += sum;
+                    }
+#pragma unroll
+                    for (int x = 0; x < H; ++x) {
+                        if (F8) {
+                            ph[x][nt][0] = movmatrix(pack_half(w[x][0], w[x][1]));
+                            ph[x][nt][1] = movmatrix(pack_half(w[x][2], w[x][3]));
+                        } else {
+                            const uint32_t h0 = bf16_pair(w[x][0], w[x][1]), h1 = bf16_pair(w[x][2], w[x][3]);
+                            ph[x][nt][0] = movmatrix(h0);
+                            ph[x][nt][1] = movmatrix(h1);
+                            pl[x][nt][0] = movmatrix(bf16_pair(w[x][0] - bf16_lo(h0), w[x][1] - bf16_hi(h0)));
+                            pl[x][nt][1] = movmatrix(bf16_pair(w[x][2] - bf16_lo(h1), w[x][3] - bf16_hi(h1)));
+                        }
+                    }
+                }
+                // O^T += V^T P^T
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    const uint32_t vs = cur + x * V::kBytes;
+                    const int keyx = key0 + x * kTileKeys;
+                    uint32_t v[V::kChunks][4][4];
+#pragma unroll
+                    for (int u = 0; u < V::kChunks; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) V::load(vs, j, u, lane, v[u][j]);
+                    // A row that does not see a key must not meet its values even with weight 0 (0 * inf
+                    // and 0 * NaN are NaN): where such a tile holds values that are not finite, each query
+                    // position is done by itself with the keys behind its limit cleared.
+                    bool slow = false;
+                    if (edge && least < len) {
+                        bool odd = false;
+#pragma unroll
+                        for (int u = 0; u < V::kChunks; ++u)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int w = 0; w < V::kLoad / 4; ++w)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += F8 ? 8 : 16)
+                                        odd |= F8 ? ((v[u][j][w] >> e) & 0x7fu) == 0x7fu
+                                                  : ((v[u][j][w] >> e) & 0x7f80u) == 0x7f80u;
+                        slow = __any_sync(0xffffffffu, odd);
+                    }
+                    auto fragment = [&](int mt, uint32_t* a, const uint32_t* mask) {
+                        // m-tile mt: columns 2y, 2y + 1 of the lane's elements of chunk u
+                        const int u = mt / (V::kElems / 2), y = mt % (V::kElems / 2);
+                        const int w = F8 ? y >> 1 : y;
+                        uint32_t k0 = v[u][0][w], k1 = v[u][1][w], k2 = v[u][2][w], k3 = v[u][3][w];
+                        if (mask) {
+                            k0 &= mask[0];
+                            k1 &= mask[1];
+                            k2 &= mask[2];
+                            k3 &= mask[3];
+                        }
+                        if (F8) {
+                            const uint32_t sel = (y & 1) ? 0x7362u : 0x5140u;
+                            const uint32_t lo = __byte_perm(k0, k1, sel), hi = __byte_perm(k2, k3, sel);
+                            a[0] = e4m3x2_half2(lo);
+                            a[1] = e4m3x2_half2(lo >> 16);
+                            a[2] = e4m3x2_half2(hi);
+                            a[3] = e4m3x2_half2(hi >> 16);
+                        } else {
+                            a[0] = __byte_perm(k0, k1, 0x5410);
+                            a[1] = __byte_perm(k0, k1, 0x7632);
+                            a[2] = __byte_perm(k2, k3, 0x5410);
+                            a[3] = __byte_perm(k2, k3, 0x7632);
+                        }
+                    };
+                    if (!slow) {
+#pragma unroll
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            uint32_t a[4];
+                            fragment(mt, a, nullptr);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<F8>(o[mt][nt], a[0], a[1], a[2], a[3], ph[x][nt][0], ph[x][nt][1]);
+                                if (!F8) mma16816<F8>(o[mt][nt], a[0], a[1], a[2], a[3], pl[x][nt][0], pl[x][nt][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int i0 = 0; i0 < p.NQ; ++i0) {
+                            uint32_t mask[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mask[j] = keyx + V::key(j, t) < least + i0 ? ~0u : 0u;
+#pragma unroll
+                            for (int mt = 0; mt < D / 16; ++mt) {
+                                uint32_t a[4];
+                                fragment(mt, a, mask);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816<F8>(c, a[0], a[1], a[2], a[3], ph[x][nt][0], ph[x][nt][1]);
+                                    if (!F8) mma16816<F8>(c, a[0], a[1], a[2], a[3], pl[x][nt][0], pl[x][nt][1]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        if (limit(nt, k & 1) == least + i0) o[mt][nt][k] += c[k];
+                                }
+                            }
                         }
                     }
                 }
             }
+            advance();
         }
         cp_wait<0>();
         __syncwarp();
 
-        // the warps' states, joined in their stages
+        // the warps' states, joined in their slots
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -432,7 +545,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
                 if (g == 0) {
                     float* e = stats + warp * 3 * C::kRows + nt * 8 + 2 * t + j;
                     e[0] = m[nt][j];
-                    e[C::kRows] = F8 ? mv[nt][j] : m[nt][j];
+                    e[C::kRows] = F8 ? r[nt][j] : m[nt][j];
                     e[2 * C::kRows] = x;
                 }
             }
@@ -453,28 +566,28 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
         float* part = p.part + ((size_t)blockIdx.x * 2 + (pos == g0 ? 0 : 1)) * C::kPart;
         const int rows = min(C::kRows, p.rows - row0);
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kPagedThreads) {
-            const int r = idx / (D / 4), c = idx % (D / 4);
+            const int i = idx / (D / 4), c = idx % (D / 4);
             float M = kNoMax, MV = kNoMax, L = 0.f;
 #pragma unroll
             for (int w = 0; w < kPagedWarps; ++w) {
-                M = fmaxf(M, stats[(w * 3) * C::kRows + r]);
-                MV = fmaxf(MV, stats[(w * 3 + 1) * C::kRows + r]);
+                M = fmaxf(M, stats[(w * 3) * C::kRows + i]);
+                MV = fmaxf(MV, stats[(w * 3 + 1) * C::kRows + i]);
             }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kPagedWarps; ++w) {
-                const float f = ex2(stats[(w * 3) * C::kRows + r] - M), fv = ex2(stats[(w * 3 + 1) * C::kRows + r] - MV);
-                L = fmaf(stats[(w * 3 + 2) * C::kRows + r], f, L);
-                const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kWarp + (r * C::kStride + 4 * c) * 4);
+                const float f = ex2(stats[(w * 3) * C::kRows + i] - M), fv = ex2(stats[(w * 3 + 1) * C::kRows + i] - MV);
+                L = fmaf(stats[(w * 3 + 2) * C::kRows + i], f, L);
+                const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kWarp + (i * C::kStride + 4 * c) * 4);
                 acc.x = fmaf(x.x, fv, acc.x);
                 acc.y = fmaf(x.y, fv, acc.y);
                 acc.z = fmaf(x.z, fv, acc.z);
                 acc.w = fmaf(x.w, fv, acc.w);
             }
             if (whole) {
-                attn_finish<D>(p, qrow + row0 + r, c, acc, M, MV, L);
+                attn_finish<D>(p, qrow + row0 + i, c, acc, M, MV, L);
             } else {
-                float* to = part + r * C::kStride;
+                float* to = part + i * C::kStride;
                 *reinterpret_cast<float4*>(to + 4 * c) = acc;
                 if (c == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, MV, L, 0.f);
             }
@@ -487,7 +600,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
             do {
                 len = seq_len(p, ++b);
             } while (len == 0);
-            units = (len + kUnitKeys - 1) / kUnitKeys;
+            units = (len + C::kUnit - 1) / C::kUnit;
         }
     }
 }
@@ -495,22 +608,22 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_attn_kernel(c
 // Joins the partial states of the segments that were cut.  Block x looks at the boundary
 // between the shares of CTAs x and x + 1 and takes the segment that is cut there for the first
 // time; blockIdx.y and gridDim.y deal out its rows.  The four warps take every fourth state.
-template <int D, int NT>
+template <int D, int NT, int UNIT>
 __global__ void __launch_bounds__(kPagedThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
     constexpr int kRows = 8 * NT, kStride = D + 4, kPart = kRows * kStride;
     __shared__ int red[8];
     __shared__ float st[kPagedWarps][4];
     __shared__ float4 ac[kPagedWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int total = plan_total(p, red);
+    const int total = plan_total<UNIT>(p, red);
     const int share = plan_share(p, total);
     const long long cut = (long long)(blockIdx.x + 1) * share;
     int b = 0, base = 0;
     const bool in = cut < total;
-    if (in) plan_locate(p, (int)cut, red, b, base);
+    if (in) plan_locate<UNIT>(p, (int)cut, red, b, base);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!in) return;
-    const int units = seq_units(p, b);
+    const int units = seq_units<UNIT>(p, b);
     const int seg = ((int)cut - base) / units, s0 = base + seg * units;
     if (s0 == (int)cut || s0 / share != (int)blockIdx.x) return;   // not cut here, or cut before
     const int c0 = s0 / share, c1 = (s0 + units - 1) / share;

@@ -4,7 +4,7 @@
 
 namespace {
 
-constexpr int kPagedCtasPerSm = 2;
+constexpr int kPagedMaxCtas = 4;     // most resident CTAs per SM of any variant
 
 int page_shift_of(int n) {
     int s = 0;
@@ -12,8 +12,8 @@ int page_shift_of(int n) {
     return s;
 }
 
-// Blocks of 8, 16 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
-int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Blocks of 8, 16, 24 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
+int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
 int check_cache(const streamkl_cache* c, bool values) {
     if (!c || !c->k || (values && !c->v)) return STREAMKL_ERR_INVALID_ARG;
@@ -22,6 +22,7 @@ int check_cache(const streamkl_cache* c, bool values) {
     if (c->type == STREAMKL_CACHE_E4M3 && (!c->k_exp || (values && !c->v_exp))) return STREAMKL_ERR_INVALID_ARG;
     if (c->d != 64 && c->d != 128) return STREAMKL_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return STREAMKL_ERR_UNSUPPORTED;
+    if ((double)c->pages * c->Hkv * c->page_size >= 2147483648.0) return STREAMKL_ERR_UNSUPPORTED;
     if (!aligned16(c->k) || !aligned16(c->k_exp) || (values && (!aligned16(c->v) || !aligned16(c->v_exp))))
         return STREAMKL_ERR_UNSUPPORTED;
     return STREAMKL_OK;
@@ -54,9 +55,10 @@ int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, co
     p.B = B; p.Hkv = c->Hkv; p.NT = NT; p.width = width; p.pages = c->pages;
     p.page_size = c->page_size;
     p.page_shift = page_shift_of(c->page_size);
-    const long long warps = (long long)B * c->Hkv * ((NT + skl::kCacheRows - 1) / skl::kCacheRows);
+    const int tokens = c->d == 128 ? skl::CacheCfg<128>::kTokens : skl::CacheCfg<64>::kTokens;
+    const long long warps = (long long)B * c->Hkv * ((NT + tokens - 1) / tokens);
     const int per = skl::kCacheThreads / 32;
-    const int grid = (int)std::min<long long>((warps + per - 1) / per, 8ll * num_sms());
+    const int grid = (int)((warps + per - 1) / per);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool f8 = c->type == STREAMKL_CACHE_E4M3;
 #define SKL_CACHE(D, F8)                                                                          \
@@ -82,7 +84,7 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     const long long rows = (long long)(Hq / c->Hkv) * NQ;
     const int nt = paged_row_tiles(rows);
     const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
-    const long long most = ((long long)width * c->page_size + skl::kUnitKeys - 1) / skl::kUnitKeys;
+    const long long most = ((long long)width * c->page_size + 63) / 64;   // the smallest unit
     if ((double)B * c->Hkv * (double)rblocks * (double)most >= 2147483648.0) return STREAMKL_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < streamkl_paged_workspace_bytes(B, Hq, c->Hkv, NQ, c->d))
         return STREAMKL_ERR_INVALID_ARG;
@@ -98,7 +100,6 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     p->page_shift = page_shift_of(c->page_size);
     p->causal = causal ? 1 : 0;
     p->min_units = 1;
-    p->grid = kPagedCtasPerSm * num_sms();
     p->sl2 = scale * 1.4426950408889634f;
     p->part = static_cast<float*>(workspace);
     return STREAMKL_OK;
@@ -121,8 +122,10 @@ int launch_join(K kernel, const skl::PagedParams& p, int gy, cudaStream_t st, co
 }
 
 template <int D, bool F8, int NT>
-int launch_paged_attn(const skl::PagedParams& p, cudaStream_t st) {
+int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     using C = skl::AttnCfg<D, F8, NT>;
+    static_assert(C::kCtas <= kPagedMaxCtas, "workspace");
+    p.grid = C::kCtas * num_sms();
     auto kern = skl::streamkl_paged_attn_kernel<D, F8, NT>;
     int rc = set_smem(kern, C::kSmem);
     if (rc) return rc;
@@ -132,7 +135,7 @@ int launch_paged_attn(const skl::PagedParams& p, cudaStream_t st) {
     // few segments: each has many partial states, and its rows go to CTAs of their own
     const long long segments = (long long)p.B * p.Hkv * p.rblocks;
     const int gy = segments * 4 <= p.grid ? std::min(p.rows, 8 * NT) : 1;
-    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT>, p, gy, st, "streamkl_paged_attn join launch");
+    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, p, gy, st, "streamkl_paged_attn join launch");
 }
 
 template <int D, bool F8>
@@ -140,20 +143,22 @@ int launch_paged_attn_rows(const skl::PagedParams& p, cudaStream_t st) {
     switch (paged_row_tiles(p.rows)) {
         case 1: return launch_paged_attn<D, F8, 1>(p, st);
         case 2: return launch_paged_attn<D, F8, 2>(p, st);
+        case 3: return launch_paged_attn<D, F8, 3>(p, st);
         default: return launch_paged_attn<D, F8, 4>(p, st);
     }
 }
 
 template <int D, bool F1, bool F2, bool SHARED, int NT>
-int launch_paged_kl(const skl::PagedParams& p, cudaStream_t st) {
+int launch_paged_kl(skl::PagedParams p, cudaStream_t st) {
     using C = skl::KlCfg<D, F1, F2, SHARED, NT>;
+    p.grid = 2 * num_sms();
     auto kern = skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>;
     int rc = set_smem(kern, C::kSmem);
     if (rc) return rc;
     kern<<<p.grid, skl::kPagedThreads, C::kSmem, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_kl launch");
-    return launch_join(skl::streamkl_paged_kl_join_kernel<NT>, p, 1, st, "streamkl_paged_kl join launch");
+    return launch_join(skl::streamkl_paged_kl_join_kernel<NT, C::kUnit>, p, 1, st, "streamkl_paged_kl join launch");
 }
 
 template <int D, bool F1, bool F2, bool SHARED>
@@ -161,6 +166,7 @@ int launch_paged_kl_rows(const skl::PagedParams& p, cudaStream_t st) {
     switch (paged_row_tiles(p.rows)) {
         case 1: return launch_paged_kl<D, F1, F2, SHARED, 1>(p, st);
         case 2: return launch_paged_kl<D, F1, F2, SHARED, 2>(p, st);
+        case 3: return launch_paged_kl<D, F1, F2, SHARED, 3>(p, st);
         default: return launch_paged_kl<D, F1, F2, SHARED, 4>(p, st);
     }
 }
@@ -189,7 +195,7 @@ int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int wid
 size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d) {
     if (B < 1 || Hq < 1 || Hkv < 1 || NQ < 1 || Hq % Hkv || (d != 64 && d != 128)) return 0;
     const long long rows = (long long)(Hq / Hkv) * NQ;
-    return (size_t)kPagedCtasPerSm * num_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
+    return (size_t)kPagedMaxCtas * num_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
 }
 
 int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,

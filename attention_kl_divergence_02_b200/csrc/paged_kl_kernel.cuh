@@ -26,6 +26,7 @@ template <int D, bool F1, bool F2, bool SHARED, int NT>
 struct KlCfg {
     using K1 = KeyTile<D, F1>;
     using K2 = KeyTile<D, F2>;
+    static constexpr int kUnit = kPagedWarps * kTileKeys;
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
     static constexpr int kOff2 = K1::kBytes;
@@ -76,7 +77,7 @@ __device__ __forceinline__ void tile_scores(uint32_t ks, int lane, const uint2* 
     constexpr int kSteps = D / 16;
 #pragma unroll
     for (int u = 0; u < K::kChunks; ++u) {
-        const uint4 x = lds128(ks + u * 512 + lane * 16), y = lds128(ks + (K::kChunks + u) * 512 + lane * 16);
+        const uint4 x = K::load(ks, 0, u, lane), y = K::load(ks, 1, u, lane);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int w = 0; w < K::kSteps; ++w) {
@@ -125,14 +126,14 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
         }
     }
 
-    const int total = plan_total(p, red);
+    const int total = plan_total<C::kUnit>(p, red);
     const int share = plan_share(p, total);
     const long long first = (long long)blockIdx.x * share;
     if (first >= total) return;
     const int g0 = (int)first, g1 = (int)min((long long)total, first + share);
     int b, base;
-    plan_locate(p, g0, red, b, base);
-    int len = seq_len(p, b), units = (len + kUnitKeys - 1) / kUnitKeys;
+    plan_locate<C::kUnit>(p, g0, red, b, base);
+    int len = seq_len(p, b), units = (len + C::kUnit - 1) / C::kUnit;
 
     for (int pos = g0; pos < g1;) {
         const int off = pos - base, seg = off / units, u0 = off - seg * units;
@@ -141,11 +142,11 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
         const int row0 = rb * C::kRows;
         const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)b * p.width;
-        const int key00 = u0 * kUnitKeys + warp * kTileKeys;
+        const int key00 = u0 * C::kUnit + warp * kTileKeys;
         uint32_t bad = 0;
 
         auto issue = [&](int i, int s) {
-            const int key0 = key00 + i * kUnitKeys;
+            const int key0 = key00 + i * C::kUnit;
             const uint32_t dst = stage0 + s * C::kStage;
             bad &= ~(1u << s);
             if (key0 < len) {
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
             else cp_commit();
             cp_wait<C::kStages - 1>();
             __syncwarp();
-            const int key0 = key00 + i * kUnitKeys;
+            const int key0 = key00 + i * C::kUnit;
             if (key0 >= len || ((bad >> st) & 1u)) continue;
             const uint32_t ks = stage0 + st * C::kStage;
 
@@ -322,27 +323,27 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
             do {
                 len = seq_len(p, ++b);
             } while (len == 0);
-            units = (len + kUnitKeys - 1) / kUnitKeys;
+            units = (len + C::kUnit - 1) / C::kUnit;
         }
     }
 }
 
 // Joins the partial states of the segments that were cut; see streamkl_paged_attn_join_kernel.
 // A warp takes a row and its lanes the states.
-template <int NT>
+template <int NT, int UNIT>
 __global__ void __launch_bounds__(kPagedThreads) streamkl_paged_kl_join_kernel(const PagedParams p) {
     constexpr int kRows = 8 * NT, kPart = kRows * 5;
     __shared__ int red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int total = plan_total(p, red);
+    const int total = plan_total<UNIT>(p, red);
     const int share = plan_share(p, total);
     const long long cut = (long long)(blockIdx.x + 1) * share;
     int b = 0, base = 0;
     const bool in = cut < total;
-    if (in) plan_locate(p, (int)cut, red, b, base);
+    if (in) plan_locate<UNIT>(p, (int)cut, red, b, base);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!in) return;
-    const int units = seq_units(p, b);
+    const int units = seq_units<UNIT>(p, b);
     const int seg = ((int)cut - base) / units, s0 = base + seg * units;
     if (s0 == (int)cut || s0 / share != (int)blockIdx.x) return;
     const int c0 = s0 / share, c1 = (s0 + units - 1) / share;

@@ -236,7 +236,7 @@ typedef struct streamkl_cache {
     uint8_t* k_exp;   /* e4m3: [pages, Hkv, page_size], a row's scale is 2^(byte - 127) */
     uint8_t* v_exp;   /*       (bf16: not used, may be NULL) */
     int type;         /* STREAMKL_CACHE_* */
-    int pages;
+    int pages;        /* pages * Hkv * page_size below 2^31 rows */
     int page_size;    /* a power of two, 16 to 1024 */
     int Hkv;
     int d;            /* 64 or 128 */
@@ -268,7 +268,7 @@ int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int wid
 
 /*
  * Bytes of workspace for streamkl_paged_attn and streamkl_paged_kl: two partial states per CTA of a
- * grid of two per SM of the current device, whatever the lengths are.  Returns 0 for sizes
+ * grid of four per SM of the current device, whatever the lengths are.  Returns 0 for sizes
  * outside the supported range.
  */
 size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);

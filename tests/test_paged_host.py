@@ -139,7 +139,7 @@ def test_caches_that_do_not_match(kw, want):
 
 
 def test_workspace_bytes():
-    n = 2 * binding.streamkl_num_sms() * 2
+    n = 4 * binding.streamkl_num_sms() * 2
     assert binding.streamkl_paged_workspace_bytes(1, 8, 8, 1, 128) == n * 8 * 132 * 4
     assert binding.streamkl_paged_workspace_bytes(64, 32, 8, 3, 64) == n * 16 * 68 * 4
     assert binding.streamkl_paged_workspace_bytes(1, 32, 1, 9, 64) == n * 32 * 68 * 4
