@@ -428,6 +428,11 @@ def bwd(mode, q1, k1, q2, k2, kl, lse1, lse2, dkl, scale=None, causal=False, out
 
 
 # ------------------------------------------------------------------ paged key-value cache
+# torch, from the first PagedCache on: these calls are made once per token, and an import statement, a
+# tuple or a device object in each check adds up to the time of a kernel.
+_torch = None
+
+
 class PagedCache:
     """The pages of a key-value cache: k and v [pages, Hkv, page_size, d], bf16 or float8_e4m3fn; with
     e4m3, k_exp and v_exp uint8 [pages, Hkv, page_size] (a row's scale is 2^(byte - 127)).  v may be
@@ -435,7 +440,9 @@ class PagedCache:
     them; page tables, lengths and positions are the caller's int32 tensors."""
 
     def __init__(self, k, v=None, k_exp=None, v_exp=None):
+        global _torch
         import torch
+        _torch = torch
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not k.is_cuda:
             raise ValueError("k must be a bf16 or float8_e4m3fn CUDA tensor [pages, Hkv, page_size, d]")
         quantised = k.dtype == torch.float8_e4m3fn
@@ -456,8 +463,10 @@ class PagedCache:
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.shape = (pages, Hkv, page_size, d)
         self.device = k.device
+        self.index = k.get_device()
         self.struct = CacheStruct(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp),
                                   CACHE_E4M3 if quantised else CACHE_BF16, pages, page_size, Hkv, d)
+        self.ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, pages, Hkv, page_size, d, quantised=False, values=True, device="cuda"):
@@ -483,21 +492,20 @@ def paged_workspace(B, Hq, Hkv, NQ, d, device="cuda"):
     return torch.empty(nbytes // 4, dtype=torch.float32, device=device)
 
 
-def _enter(device, stream):
-    """(guard, stream handle) of a call on `device`: what the call allocates belongs to the stream it
-    runs on, the caller's `stream` (an object or a handle) or the device's current one."""
-    import torch
+def _enter(cache, stream):
+    """(guard, stream handle) of a call on a cache's device: what the call allocates belongs to the stream
+    it runs on, the caller's `stream` (an object or a handle) or the device's current one."""
     if stream is None:
         guard = None
-        if device.index != torch.cuda.current_device():
-            guard = torch.cuda.device(device)
+        if cache.index != _torch.cuda.current_device():
+            guard = _torch.cuda.device(cache.device)
             guard.__enter__()
-        return guard, torch._C._cuda_getCurrentRawStream(device.index)
+        return guard, _torch._C._cuda_getCurrentRawStream(cache.index)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-    if stream.device != device:
-        raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, device))
-    guard = torch.cuda.stream(stream)
+        stream = _torch.cuda.ExternalStream(stream, cache.device) if stream else _torch.cuda.default_stream(cache.device)
+    if stream.device != cache.device:
+        raise ValueError("the stream is on %s, the cache is on %s" % (stream.device, cache.device))
+    guard = _torch.cuda.stream(stream)
     guard.__enter__()
     return guard, stream.cuda_stream
 
@@ -507,42 +515,46 @@ def _leave(guard):
         guard.__exit__(None, None, None)
 
 
-def _check_ints(name, t, shape, device):
-    import torch
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s (got %s %s on %s)"
-                         % (name, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+def _need(name, t, dtype, shape, cache):
+    """Refuses a tensor that the kernels would misread; `shape` is a tuple."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s on %s)"
+                         % (name, dtype, shape, cache.device, t.dtype, tuple(t.shape), t.device))
 
 
-def _check_paging(cache, table, B):
+def _width(table, B, cache):
+    """Pages of a row of the table [B, width]."""
     if table.dim() != 2 or table.shape[1] < 1:
         raise ValueError("table must be int32 [B, width]")
-    _check_ints("table", table, (B, table.shape[1]), cache.device)
+    width = table.shape[1]
+    _need("table", table, _torch.int32, (B, width), cache)
+    return width
 
 
-def _check_rows(cache, k, v):
-    import torch
+def _rows_shape(cache, k, v):
+    """Shape of dense rows [B, Hkv, rows, d] that fit the cache."""
+    shape = tuple(k.shape)
     if cache.v is None:
         raise ValueError("this cache has no values")
-    if k.dim() != 4 or k.shape[1] != cache.shape[1] or k.shape[3] != cache.shape[3] or k.shape[0] < 1 or k.shape[2] < 1:
-        raise ValueError("k and v must be [B, %d, rows, %d] (got %s)" % (cache.shape[1], cache.shape[3], tuple(k.shape)))
-    _check_tensor("k", k, k.shape, torch.bfloat16, cache.device)
-    _check_tensor("v", v, k.shape, torch.bfloat16, cache.device)
+    if len(shape) != 4 or shape[1] != cache.shape[1] or shape[3] != cache.shape[3] or shape[0] < 1 or shape[2] < 1:
+        raise ValueError("k and v must be [B, %d, rows, %d] (got %s)" % (cache.shape[1], cache.shape[3], shape))
+    _need("k", k, _torch.bfloat16, shape, cache)
+    _need("v", v, _torch.bfloat16, shape, cache)
+    return shape
 
 
 def cache_append(cache, k, v, table, start, count=None, stream=None):
     """Writes k, v (bf16 [B, Hkv, NT, d]) into the cache: row i < count[b] (NT without `count`) of
     sequence b at position start[b] + i.  table int32 [B, width], start and count int32 [B]."""
-    _check_rows(cache, k, v)
-    B, _, NT, _ = k.shape
-    _check_paging(cache, table, B)
-    _check_ints("start", start, (B,), cache.device)
+    B, _, NT, _ = _rows_shape(cache, k, v)
+    width = _width(table, B, cache)
+    _need("start", start, _torch.int32, (B,), cache)
     if count is not None:
-        _check_ints("count", count, (B,), cache.device)
-    guard, handle = _enter(cache.device, stream)
+        _need("count", count, _torch.int32, (B,), cache)
+    guard, handle = _enter(cache, stream)
     try:
-        rc = load().streamkl_cache_append(ctypes.byref(cache.struct), k.data_ptr(), v.data_ptr(), table.data_ptr(),
-                                          table.shape[1], start.data_ptr(), _ptr(count), B, NT, handle)
+        rc = load().streamkl_cache_append(cache.ref, k.data_ptr(), v.data_ptr(), table.data_ptr(), width, start.data_ptr(),
+                                          None if count is None else count.data_ptr(), B, NT, handle)
     finally:
         _leave(guard)
     if rc != OK:
@@ -553,25 +565,23 @@ def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=No
     """Reads rows back into (k, v), bf16 [B, Hkv, rows, d]: row i < count[b] is the cached row at position
     start[b] + i (from 0 without `start`); rows behind the count are left as they were (zeros in
     tensors allocated here)."""
-    import torch
     if out is None and (rows is None or rows < 1 or table.dim() != 2):
         raise ValueError("out, or rows of at least 1 and a table [B, width], are required")
-    guard, handle = _enter(cache.device, stream)
+    guard, handle = _enter(cache, stream)
     try:
         if out is None:
-            out = tuple(torch.zeros((table.shape[0], cache.shape[1], rows, cache.shape[3]), dtype=torch.bfloat16,
-                                    device=cache.device) for _ in range(2))
+            out = tuple(_torch.zeros((table.shape[0], cache.shape[1], rows, cache.shape[3]), dtype=_torch.bfloat16,
+                                     device=cache.device) for _ in range(2))
         k, v = out
-        _check_rows(cache, k, v)
-        if rows is not None and rows != k.shape[2]:
-            raise ValueError("out has %d rows, not %d" % (k.shape[2], rows))
-        B = k.shape[0]
-        _check_paging(cache, table, B)
-        _check_ints("count", count, (B,), cache.device)
+        B, _, NT, _ = _rows_shape(cache, k, v)
+        if rows is not None and rows != NT:
+            raise ValueError("out has %d rows, not %d" % (NT, rows))
+        width = _width(table, B, cache)
+        _need("count", count, _torch.int32, (B,), cache)
         if start is not None:
-            _check_ints("start", start, (B,), cache.device)
-        rc = load().streamkl_cache_gather(ctypes.byref(cache.struct), table.data_ptr(), table.shape[1], _ptr(start),
-                                          count.data_ptr(), B, k.shape[2], k.data_ptr(), v.data_ptr(), handle)
+            _need("start", start, _torch.int32, (B,), cache)
+        rc = load().streamkl_cache_gather(cache.ref, table.data_ptr(), width, None if start is None else start.data_ptr(),
+                                          count.data_ptr(), B, NT, k.data_ptr(), v.data_ptr(), handle)
     finally:
         _leave(guard)
     if rc != OK:
@@ -579,50 +589,49 @@ def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=No
     return out
 
 
-def _check_paged(cache, q, table, lengths):
-    import torch
-    shape = q.shape
+def _query_shape(name, q, cache):
+    """Shape of queries [B, Hq, NQ, d] that fit the cache."""
+    shape = tuple(q.shape)
     if len(shape) != 4 or shape[3] != cache.shape[3] or min(shape) < 1 or shape[1] % cache.shape[1]:
-        raise ValueError("q must be [B, Hq, NQ, %d], Hq a multiple of %d (got %s)"
-                         % (cache.shape[3], cache.shape[1], tuple(shape)))
-    if q.dtype is not torch.bfloat16 or q.device != cache.device or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 tensor on %s" % (cache.device,))
-    _check_paging(cache, table, shape[0])
-    _check_ints("lengths", lengths, (shape[0],), cache.device)
+        raise ValueError("%s must be [B, Hq, NQ, %d], Hq a multiple of %d (got %s)"
+                         % (name, cache.shape[3], cache.shape[1], shape))
+    _need(name, q, _torch.bfloat16, shape, cache)
+    return shape
 
 
-def _paged_scratch(workspace, B, Hq, Hkv, NQ, d, device):
-    import torch
-    need = load().streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d)
+def _scratch(workspace, shape, cache):
+    """The caller's workspace, checked, or a new one; (tensor, bytes).  The library checks its size."""
     if workspace is None:
-        return torch.empty(need // 4, dtype=torch.float32, device=device)
-    _check_workspace(workspace, need, device)
-    return workspace
+        B, Hq, NQ, d = shape
+        nbytes = streamkl_paged_workspace_bytes(B, Hq, cache.shape[1], NQ, d)
+        return _torch.empty(nbytes // 4, dtype=_torch.float32, device=cache.device), nbytes
+    if workspace.get_device() != cache.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % (cache.device,))
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def paged_attn(q, cache, table, lengths, scale=None, causal=True, out=None, workspace=None, stream=None):
     """Attention of new tokens over the cache: (out bf16 [B, Hq, NQ, d], lse fp32 [B, Hq, NQ]).  lengths int32
     [B] count the new tokens; causal: they are the last NQ and see their own past only.  `workspace`
     (paged_workspace) is allocated here when not given."""
-    import torch
-    _check_paged(cache, q, table, lengths)
+    shape = _query_shape("q", q, cache)
     if cache.v is None:
         raise ValueError("this cache has no values")
-    B, Hq, NQ, d = q.shape
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    guard, handle = _enter(q.device, stream)
+    B, Hq, NQ, d = shape
+    width = _width(table, B, cache)
+    _need("lengths", lengths, _torch.int32, (B,), cache)
+    guard, handle = _enter(cache, stream)
     try:
         if out is None:
-            out = (torch.empty_like(q), torch.empty((B, Hq, NQ), dtype=torch.float32, device=q.device))
+            o, lse = out = _torch.empty_like(q), _torch.empty((B, Hq, NQ), dtype=_torch.float32, device=cache.device)
         else:
-            _check_tensor("out", out[0], q.shape, torch.bfloat16, q.device)
-            _check_tensor("lse", out[1], (B, Hq, NQ), torch.float32, q.device)
-        workspace = _paged_scratch(workspace, B, Hq, cache.shape[1], NQ, d, q.device)
-        rc = load().streamkl_paged_attn(ctypes.byref(cache.struct), q.data_ptr(), table.data_ptr(), table.shape[1],
-                                        lengths.data_ptr(), B, Hq, NQ, scale, 1 if causal else 0,
-                                        out[0].data_ptr(), out[1].data_ptr(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), handle)
+            o, lse = out
+            _need("out", o, _torch.bfloat16, shape, cache)
+            _need("lse", lse, _torch.float32, (B, Hq, NQ), cache)
+        workspace, nbytes = _scratch(workspace, shape, cache)
+        rc = load().streamkl_paged_attn(cache.ref, q.data_ptr(), table.data_ptr(), width, lengths.data_ptr(), B, Hq, NQ,
+                                        d ** -0.5 if scale is None else scale, 1 if causal else 0, o.data_ptr(),
+                                        lse.data_ptr(), workspace.data_ptr(), nbytes, handle)
     finally:
         _leave(guard)
     if rc != OK:
@@ -634,29 +643,27 @@ def paged_kl(q1, cache1, q2, cache2, table, lengths, scale=None, causal=True, ou
     """KL(P1 || P2) of two attentions of the new tokens over paged key caches: (kl, lse1, lse2), fp32
     [B, Hq, NQ].  P1 from q1 and cache1's keys, P2 from q2 and cache2's; pass the same cache twice
     for shared keys.  Other arguments as paged_attn."""
-    import torch
-    _check_paged(cache1, q1, table, lengths)
-    if q1.shape != q2.shape or cache1.shape != cache2.shape or cache1.device != cache2.device:
-        raise ValueError("both sides must agree in shape and device (q %s and %s, caches %s and %s)"
-                         % (tuple(q1.shape), tuple(q2.shape), cache1.shape, cache2.shape))
-    if q2.dtype is not torch.bfloat16 or q2.device != q1.device or not q2.is_contiguous():
-        raise ValueError("q2 must be a contiguous bf16 tensor on %s" % (q1.device,))
-    B, Hq, NQ, d = q1.shape
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    guard, handle = _enter(q1.device, stream)
+    shape = _query_shape("q1", q1, cache1)
+    if cache1.shape != cache2.shape or cache1.index != cache2.index:
+        raise ValueError("both caches must agree in shape and device (%s on %s, %s on %s)"
+                         % (cache1.shape, cache1.device, cache2.shape, cache2.device))
+    _need("q2", q2, _torch.bfloat16, shape, cache1)
+    B, Hq, NQ, d = shape
+    width = _width(table, B, cache1)
+    _need("lengths", lengths, _torch.int32, (B,), cache1)
+    guard, handle = _enter(cache1, stream)
     try:
         if out is None:
-            out = tuple(torch.empty((B, Hq, NQ), dtype=torch.float32, device=q1.device) for _ in range(3))
+            out = _torch.empty((3, B, Hq, NQ), dtype=_torch.float32, device=cache1.device).unbind(0)
         else:
             for name, o in zip(("kl", "lse1", "lse2"), out):
-                _check_tensor(name, o, (B, Hq, NQ), torch.float32, q1.device)
-        workspace = _paged_scratch(workspace, B, Hq, cache1.shape[1], NQ, d, q1.device)
-        rc = load().streamkl_paged_kl(ctypes.byref(cache1.struct), q1.data_ptr(), ctypes.byref(cache2.struct),
-                                      q2.data_ptr(), table.data_ptr(), table.shape[1], lengths.data_ptr(), B, Hq, NQ,
-                                      scale, 1 if causal else 0, out[0].data_ptr(), out[1].data_ptr(),
-                                      out[2].data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), handle)
+                _need(name, o, _torch.float32, (B, Hq, NQ), cache1)
+        kl, lse1, lse2 = out
+        workspace, nbytes = _scratch(workspace, shape, cache1)
+        rc = load().streamkl_paged_kl(cache1.ref, q1.data_ptr(), cache2.ref, q2.data_ptr(), table.data_ptr(), width,
+                                      lengths.data_ptr(), B, Hq, NQ, d ** -0.5 if scale is None else scale,
+                                      1 if causal else 0, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
+                                      workspace.data_ptr(), nbytes, handle)
     finally:
         _leave(guard)
     if rc != OK:

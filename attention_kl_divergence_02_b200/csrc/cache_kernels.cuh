@@ -169,8 +169,10 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_gather_kernel(co
         uint4 y = x[r];
         if (F8) {
             const float s = exp_scale(__shfl_sync(0xffffffffu, exponent, r, C::kLanes));
-            const float2 v0 = half2_floats(e4m3x2_half2(x[r].x)), v1 = half2_floats(e4m3x2_half2(x[r].x >> 16));
-            const float2 v2 = half2_floats(e4m3x2_half2(x[r].y)), v3 = half2_floats(e4m3x2_half2(x[r].y >> 16));
+            uint32_t h[4];
+            e4m3x4_half2(x[r].x, h[0], h[1]);
+            e4m3x4_half2(x[r].y, h[2], h[3]);
+            const float2 v0 = half2_floats(h[0]), v1 = half2_floats(h[1]), v2 = half2_floats(h[2]), v3 = half2_floats(h[3]);
             y = make_uint4(bf16_pair(v0.x * s, v0.y * s), bf16_pair(v1.x * s, v1.y * s), bf16_pair(v2.x * s, v2.y * s),
                            bf16_pair(v3.x * s, v3.y * s));
         }

@@ -13,7 +13,8 @@
 // CTA stores a partial state, and a second kernel joins the partial states of a segment in
 // the order of its CTAs (no atomics: the same inputs give the same bits).  A CTA has at most two
 // partial segments, its first (slot 2c) and its last (slot 2c + 1), so the workspace depends on
-// the grid alone and not on the lengths.
+// the grid alone and not on the lengths.  Where the page table is so narrow that every segment is short,
+// segments are dealt out whole, and there is nothing to join.
 #pragma once
 
 #include "sm100.cuh"
@@ -28,6 +29,11 @@ constexpr int kPagedThreads = 128;     // 4 warps, each with its own tiles and c
 constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kTileKeys = 16;          // keys of a product (its M)
 constexpr float kNoMax = -3.402823466e38f;   // running maximum before any key
+// Running sums refer to 2^m with m within kSlack (log2 units) of the running maximum, and are rescaled only
+// when it grows beyond that: weights reach 2^8, which costs fp32 sums and the weights' 16-bit types
+// (relative rounding, fp16 up to 2^15) nothing, and the rescaling, in almost every turn of a short
+// sequence with many rows otherwise, all but vanishes.
+constexpr float kSlack = 8.f;
 
 struct PagedPool {
     const uint8_t* rows;
@@ -45,7 +51,7 @@ struct PagedParams {
     int rblocks;           // blocks of query rows
     int width, pages, page_size, page_shift;
     int causal;
-    int min_units;         // least share of a CTA
+    int whole;             // segments are not cut: no partial states
     int grid;              // CTAs of the main kernel
     float sl2;             // scale * log2(e)
     uint16_t* out;         // attention
@@ -67,68 +73,142 @@ __device__ __forceinline__ int seq_units(const PagedParams& p, int b) {
     return (seq_len(p, b) + UNIT - 1) / UNIT;
 }
 
-// Sum of x over the CTA's 128 threads, in every thread.  red: 4 ints.
-__device__ __forceinline__ int block_sum(int x, int* red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    return red[0] + red[1] + red[2] + red[3];
-}
-
-// T: units of all segments.
+// T: units of all segments.  Each warp computes it by itself, as the rest of the plan: 32 sequences at a
+// time, without a barrier.
 template <int UNIT>
-__device__ __forceinline__ int plan_total(const PagedParams& p, int* red) {
+__device__ __forceinline__ int plan_total(const PagedParams& p) {
     int n = 0;
-    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) n += seq_units<UNIT>(p, b);
-    return block_sum(n, red) * p.Hkv * p.rblocks;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) n += seq_units<UNIT>(p, b);
+    return __reduce_add_sync(0xffffffffu, n) * p.Hkv * p.rblocks;
 }
 
 // The share of a CTA.
 __device__ __forceinline__ int plan_share(const PagedParams& p, int total) {
-    return max((total + p.grid - 1) / p.grid, p.min_units);
+    return max((total + p.grid - 1) / p.grid, 1);
 }
 
 // The sequence that holds unit g (0 <= g < T), and the first unit of that sequence.
-// red: 8 ints.  Called by all 128 threads.
 template <int UNIT>
-__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int* red, int& b, int& base) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = p.Hkv * p.rblocks;
+__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int& b, int& base) {
+    const int lane = threadIdx.x & 31, per = p.Hkv * p.rblocks;
     int before = 0;
-    __syncthreads();
-    for (int b0 = 0; b0 < p.B; b0 += kPagedThreads) {
-        const int bi = b0 + threadIdx.x;
-        const int x = bi < p.B ? seq_units<UNIT>(p, bi) * per : 0;
-        int incl = x;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int x = b0 + lane < p.B ? seq_units<UNIT>(p, b0 + lane) * per : 0;
+        int upto = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        if (lane == 31) red[warp] = incl;
-        __syncthreads();
-        int off = before;
-        for (int w = 0; w < warp; ++w) off += red[w];
-        const int all = red[0] + red[1] + red[2] + red[3];
-        incl += off;
-        if (x > 0 && g >= incl - x && g < incl) {
-            red[4] = bi;
-            red[5] = incl - x;
+        const unsigned behind = __ballot_sync(0xffffffffu, g < before + upto);
+        if (behind) {
+            const int at = __ffs(behind) - 1;
+            b = b0 + at;
+            base = before + __shfl_sync(0xffffffffu, upto - x, at);
+            return;
         }
-        __syncthreads();
-        if (g < before + all) break;
-        before += all;
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    b = red[4];
-    base = red[5];
+    b = base = 0;      // not reached for g < T
 }
+
+// A CTA's walk over its work: whole segments in turn where all are short (p.whole), else its share of
+// all units, cut where it begins and ends.
+template <int UNIT>
+struct PagedWalk {
+    int b, len, seg, units, u0, n;     // sequence, its keys, segment in it, its units, first unit and number of them to do
+    int pos, base, end, first;
+
+    __device__ __forceinline__ bool start(const PagedParams& p) {
+        if (p.whole) {
+            pos = (int)blockIdx.x;
+            end = p.B * p.Hkv * p.rblocks;
+            return find_whole(p);
+        }
+        const int total = plan_total<UNIT>(p), share = plan_share(p, total);
+        const long long at = (long long)blockIdx.x * share;
+        if (at >= total) return false;
+        first = pos = (int)at;
+        end = (int)min((long long)total, at + share);
+        plan_locate<UNIT>(p, pos, b, base);
+        len = seq_len(p, b);
+        units = (len + UNIT - 1) / UNIT;
+        cut();
+        return true;
+    }
+    __device__ __forceinline__ bool next(const PagedParams& p) {
+        if (p.whole) {
+            pos += gridDim.x;
+            return find_whole(p);
+        }
+        pos += n;
+        if (pos >= end) return false;
+        if (pos - base == units * p.Hkv * p.rblocks) {
+            base = pos;
+            do {
+                len = seq_len(p, ++b);
+            } while (len == 0);
+            units = (len + UNIT - 1) / UNIT;
+        }
+        cut();
+        return true;
+    }
+    __device__ __forceinline__ bool complete() const { return n == units; }
+    __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (pos == first ? 0 : 1); }
+
+private:
+    __device__ __forceinline__ void cut() {
+        const int off = pos - base;
+        seg = off / units;
+        u0 = off - seg * units;
+        n = min(units - u0, end - pos);
+    }
+    __device__ __forceinline__ bool find_whole(const PagedParams& p) {
+        const int per = p.Hkv * p.rblocks;
+        for (; pos < end; pos += gridDim.x) {
+            b = pos / per;
+            seg = pos - b * per;
+            len = seq_len(p, b);
+            if (len > 0) {
+                n = units = (len + UNIT - 1) / UNIT;
+                u0 = 0;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+// The segment that is cut for the first time between the shares of CTAs `block` and `block` + 1.
+template <int UNIT>
+struct PagedCut {
+    int b, seg, c0, c1, first_slot;    // its CTAs c0 .. c1; slot of c0's partial state (2c for the others)
+
+    __device__ __forceinline__ bool find(const PagedParams& p, int block) {
+        const int total = plan_total<UNIT>(p), share = plan_share(p, total);
+        const long long cut = (long long)(block + 1) * share;
+        if (cut >= total) return false;
+        int base;
+        plan_locate<UNIT>(p, (int)cut, b, base);
+        const int units = seq_units<UNIT>(p, b);
+        seg = ((int)cut - base) / units;
+        const int s0 = base + seg * units;
+        if (s0 == (int)cut || s0 / share != block) return false;    // not cut here, or cut before
+        c0 = block;
+        c1 = (s0 + units - 1) / share;
+        first_slot = 2 * c0 + (s0 == c0 * share ? 0 : 1);
+        return true;
+    }
+    __device__ __forceinline__ int slot(int c) const { return c == c0 ? first_slot : 2 * c; }
+};
 
 // ------------------------------------------------------------------ warp-level pieces
 // 16 bytes from global into shared memory, `bytes` of them read, zeros behind.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -173,11 +253,10 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     return y;
 }
 
-// Two e4m3 values (the low 16 bits of x) as two fp16 values, exactly (NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t x) {
-    uint32_t y;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
-    return y;
+// Four e4m3 values as two pairs of fp16 values, exactly (NaN stays NaN).
+__device__ __forceinline__ void e4m3x4_half2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(x));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -211,31 +290,17 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 // 16 slots of a k-step stand for is free as long as K and Q agree, so the lane takes 16
 // contiguous bytes of a key row (chunk u: bytes [64u + 16t, +16)) as its slots of 2 (bf16) or 4
 // (e4m3) k-steps.  The 8 lanes of a load phase meet chunks t of two neighbouring rows.
+// Where a lane's chunk lies splits into a lane's constant, computed once per kernel, and compile-time
+// offsets; `place` states the layout, and the static functions below follow it.
 template <int D, bool F8>
 struct RowTile {
     static constexpr int kRow = D * (F8 ? 1 : 2);     // bytes of a row
     static constexpr int kRowChunks = kRow / 16;
     static constexpr int kBytes = kTileKeys * kRow;   // of a tile
-    static constexpr int kCopies = kBytes / 512;      // of a lane
+    static constexpr int kCopies = kBytes / 512;      // of a lane: copy i is 512 / kRow rows further
+    static constexpr int kStep = 512 / kRow;
 
-    // rows: the tile's first row; valid: rows of the tile that exist (none: at most 0; zeros behind them)
-    template <typename Place>
-    __device__ static __forceinline__ void copy_by(uint32_t dst, const uint8_t* rows, int valid, int lane, Place place) {
-        const uint8_t* from = rows + lane * 16;
-        if (valid >= kTileKeys) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int at = i * 32 + lane;
-                cp_async16(dst + place(at / kRowChunks, at % kRowChunks), from + i * 512, 16);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int at = i * 32 + lane;
-                cp_async16(dst + place(at / kRowChunks, at % kRowChunks), from + i * 512, at / kRowChunks < valid ? 16 : 0);
-            }
-        }
-    }
+    __device__ static __forceinline__ int copy_row(int lane) { return lane / kRowChunks; }
 };
 
 template <int D, bool F8>
@@ -248,13 +313,21 @@ struct KeyTile : RowTile<D, F8> {
     __device__ static __forceinline__ int place(int row, int chunk) {
         return row * R::kRow + ((R::kRow >= 128 ? chunk ^ ((row & 1) * 4) : chunk) * 16);
     }
-    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
-        R::copy_by(dst, rows, valid, lane, place);
+    __device__ static __forceinline__ int copy_offset(int lane) { return place(R::copy_row(lane), lane % R::kRowChunks); }
+    // dst: the tile + copy_offset; from: the tile's first row + lane * 16; valid: rows that exist (zeros behind)
+    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* from, int valid, int lane) {
+        if (valid >= kTileKeys) {
+#pragma unroll
+            for (int i = 0; i < R::kCopies; ++i) cp_async16(dst + i * 512, from + i * 512);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R::kCopies; ++i)
+                cp_async16(dst + i * 512, from + i * 512, i * R::kStep + R::copy_row(lane) < valid ? 16 : 0);
+        }
     }
-    // chunk u of key g + 8h
-    __device__ static __forceinline__ uint4 load(uint32_t src, int h, int u, int lane) {
-        return lds128(src + place((lane >> 2) + 8 * h, (lane & 3) + 4 * u));
-    }
+    // chunk u of key g + 8h lies at load_offset(lane, u & 1) + load_step(h, u)
+    __device__ static __forceinline__ int load_offset(int lane, int odd) { return place(lane >> 2, (lane & 3) + 4 * odd); }
+    __device__ static constexpr int load_step(int h, int u) { return h * 8 * R::kRow + (u >> 1) * 128; }
 };
 
 // Power of two that brings a query row's largest magnitude into [2^14, 2^15): e4m3 keys meet

@@ -2,8 +2,8 @@
 //
 //     s_j = scale <q, k_j>,   o = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
 //
-// over the keys j that the row sees, in one pass: running maximum m, sum l and weighted sum o are
-// rescaled by 2^(m_old - m_new) when the maximum grows.
+// over the keys j that the row sees, in one pass: sum l and weighted sum o refer to a running
+// maximum m and are rescaled by 2^(m_old - m_new) when it moves (see kSlack).
 //
 // Bound: every cached byte is read once and used for 2 flops per query row and element, so with the
 // few rows of a KV head (Hq / Hkv * NQ) the floor is cache bytes / HBM bandwidth.  Everything here
@@ -46,17 +46,34 @@ struct ValueTile : RowTile<D, F8> {
         if (R::kRow >= 128) return row * R::kRow + (chunk ^ (row & 6)) * 16;
         return ((row & 1) + (row >> 2) * 2) * 128 + ((row >> 1) & 1) * 64 + (chunk ^ (((row >> 2) & 1) * 2)) * 16;
     }
-    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* rows, int valid, int lane) {
-        R::copy_by(dst, rows, valid, lane, place);
+    __device__ static __forceinline__ int copy_offset(int lane) { return place(R::copy_row(lane), lane % R::kRowChunks); }
+    // as KeyTile::copy; the tile is 128-byte aligned, so a row's swizzle flips bits of the address
+    __device__ static __forceinline__ void copy(uint32_t dst, const uint8_t* from, int valid, int lane) {
+        if (valid >= kTileKeys) {
+#pragma unroll
+            for (int i = 0; i < R::kCopies; ++i) cp_async16((dst ^ flip(i)) + i * 512, from + i * 512);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R::kCopies; ++i)
+                cp_async16((dst ^ flip(i)) + i * 512, from + i * 512, i * R::kStep + R::copy_row(lane) < valid ? 16 : 0);
+        }
     }
-    // the lane's words (4 bytes) of key j, load u
-    __device__ static __forceinline__ void load(uint32_t src, int j, int u, int lane, uint32_t* w) {
-        const int row = key(j, lane & 3), g = lane >> 2;
+    __device__ static constexpr uint32_t flip(int i) { return R::kRow >= 128 ? ((i * R::kStep) & 6) * 16 : 0; }
+    // load u of key(j, t) lies at load_offset(lane) + load_step(j, u)
+    __device__ static __forceinline__ int load_offset(int lane) {
+        const int g = lane >> 2;
+        return kLoad == 16 ? place(key(0, lane & 3), g) : place(key(0, lane & 3), g >> 1) + (g & 1) * 8;
+    }
+    __device__ static constexpr int load_step(int j, int u) {
+        return R::kRow >= 128 ? ((j & 1) + 8 * (j >> 1)) * R::kRow + u * 128 : (j & 1) * 128 + (j >> 1) * 512;
+    }
+    // the lane's words (4 bytes) there
+    __device__ static __forceinline__ void load(uint32_t src, uint32_t* w) {
         if (kLoad == 16) {
-            const uint4 v = lds128(src + place(row, g + 8 * u));
+            const uint4 v = lds128(src);
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         } else {
-            const uint2 v = lds64(src + place(row, g >> 1) + (g & 1) * 8);
+            const uint2 v = lds64(src);
             w[0] = v.x; w[1] = v.y;
         }
     }
@@ -79,7 +96,7 @@ struct AttnCfg {
     // keys and values in turn; their number is odd, so that the slot refilled after a key (value) slot
     // is used again takes keys (values).
     static constexpr int kExps = H * K::kBytes;
-    static constexpr int kSlot = H * K::kBytes + (F8 ? kKeys : 0);
+    static constexpr int kSlot = H * K::kBytes + (F8 ? 128 : 0);
     static constexpr int kFit = (kCtas == 3 ? 17 : 26) * 1024 / kSlot;   // a warp's share of shared memory
     static constexpr int kSlots = kFit >= 9 ? 9 : (kFit % 2 ? kFit : kFit - 1);
     static constexpr int kAhead = (kSlots - 1) / 2;                    // tiles in flight
@@ -89,8 +106,7 @@ struct AttnCfg {
     static constexpr int kQ = kPagedWarps * kWarp;
     static constexpr int kFactor = kQ + (kSharedQ ? NT * kSteps * 32 * 8 : 0);
     static constexpr int kStats = kFactor + (kSharedQ ? NT * 32 * 4 : 0);   // [warp][3][kRows]
-    static constexpr int kRed = kStats + kPagedWarps * 3 * kRows * 4;
-    static constexpr int kSmem = kRed + 64;
+    static constexpr int kSmem = kStats + kPagedWarps * 3 * kRows * 4;
     static constexpr int kPart = kRows * kStride;                      // floats of a partial state
     static_assert(kSlots >= 3 && kSlots % 2 == 1, "ring");
     static_assert(kWarp >= kRows * kStride * 4, "a warp's state is joined in its slots");
@@ -122,8 +138,12 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     const uint32_t sb = smem_u32(smem);
     const uint32_t ring = sb + warp * C::kWarp;
     constexpr int H = C::H;
+    // where this lane copies from and to, and loads from, in every tile
+    const uint8_t *keys = p.a.rows + lane * 16, *values = p.b.rows + lane * 16;
+    const uint32_t key_to = K::copy_offset(lane), value_to = V::copy_offset(lane);
+    const uint32_t key_at[2] = {(uint32_t)K::load_offset(lane, 0), (uint32_t)K::load_offset(lane, K::kChunks > 1)};
+    const uint32_t value_at = V::load_offset(lane);
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
-    int* red = reinterpret_cast<int*>(smem + C::kRed);
 
     // sequences without keys: zeros and -inf
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -135,23 +155,14 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         for (size_t i = threadIdx.x; i < n; i += kPagedThreads) p.lse1[r0 + i] = -INFINITY;
     }
 
-    const int total = plan_total<C::kUnit>(p, red);
-    const int share = plan_share(p, total);
-    const long long first = (long long)blockIdx.x * share;
-    if (first >= total) return;
-    const int g0 = (int)first, g1 = (int)min((long long)total, first + share);
-    int b, base;
-    plan_locate<C::kUnit>(p, g0, red, b, base);
-    int len = seq_len(p, b), units = (len + C::kUnit - 1) / C::kUnit;
-
-    for (int pos = g0; pos < g1;) {
-        const int off = pos - base, seg = off / units, u0 = off - seg * units;
-        const int n = min(units - u0, g1 - pos);          // units, hence turns of a warp
-        const int h = seg / p.rblocks, rb = seg - h * p.rblocks;
+    PagedWalk<C::kUnit> walk;
+    for (bool more = walk.start(p); more; more = walk.next(p)) {
+        const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
+        const int h = walk.seg / p.rblocks, rb = walk.seg - h * p.rblocks;
         const int row0 = rb * C::kRows;
-        const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
-        const int* table = p.table + (size_t)b * p.width;
-        const int key00 = u0 * C::kUnit + warp * C::kKeys;
+        const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
+        const int* table = p.table + (size_t)walk.b * p.width;
+        const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
 
         // The turn whose rows are requested next: its pages (looked up one turn before), pool rows and
         // number of existing keys of each tile.
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         bad |= 1u << ((i & 15) * 2 + x);
                         if (lane == 0) g_page_status = 5;
                     }
-                    K::copy(dst + x * K::kBytes, p.a.rows + (size_t)row[x] * K::kRow, valid[x], lane);
+                    K::copy(dst + x * K::kBytes + key_to, keys + (size_t)row[x] * K::kRow, valid[x], lane);
                     if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.a.exps + row[x], 16);
                 }
                 look_up(i + 1);
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
             if (i < n) {
 #pragma unroll
                 for (int x = 0; x < H; ++x) {
-                    V::copy(dst + x * V::kBytes, p.b.rows + (size_t)row[x] * V::kRow, valid[x], lane);
+                    V::copy(dst + x * V::kBytes + value_to, values + (size_t)row[x] * V::kRow, valid[x], lane);
                     if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.b.exps + row[x], 16);
                 }
             }
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         };
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        // m: running maximum of the scores; r: reference of the weights (bf16: m); l: sum
+        // m: reference of the sum, within kSlack of the scores' maximum; r: of the weights (bf16: m); l: sum
         float o[D / 16][NT][4], m[NT][2], r[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -281,16 +292,15 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                 for (int u = 0; u < K::kChunks; ++u)
 #pragma unroll
                     for (int x = 0; x < H; ++x) {
-                        const uint4 y0 = K::load(cur + x * K::kBytes, 0, u, lane), y1 = K::load(cur + x * K::kBytes, 1, u, lane);
+                        const uint32_t at = cur + x * K::kBytes + key_at[u & 1];
+                        const uint4 y0 = lds128(at + K::load_step(0, u)), y1 = lds128(at + K::load_step(1, u));
                         const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
                         for (int w = 0; w < K::kSteps; ++w) {
                             uint32_t a0, a1, a2, a3;
                             if (F8) {
-                                a0 = e4m3x2_half2(w0[w]);
-                                a1 = e4m3x2_half2(w1[w]);
-                                a2 = e4m3x2_half2(w0[w] >> 16);
-                                a3 = e4m3x2_half2(w1[w] >> 16);
+                                e4m3x4_half2(w0[w], a0, a2);
+                                e4m3x4_half2(w1[w], a1, a3);
                             } else {
                                 a0 = w0[(2 * w) & 3];
                                 a1 = w1[(2 * w) & 3];
@@ -336,29 +346,25 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
             cp_wait<C::kSlots - 1>();
             __syncwarp();
             if (some) {
-                // e4m3: scales of the values, their exponents' range over the turn's keys
-                float kv[H][2];
+                // e4m3: the exponents' range over the turn's keys
                 int e_max = 0;
                 bool near = true;
                 if (F8) {
-                    uint32_t e = lds8(cur + C::kExps + (lane & (C::kKeys - 1)));
-                    const bool in = !edge || (key0 + (lane & (C::kKeys - 1)) < len &&
-                                              !((bad >> ((i & 15) * 2 + ((lane & (C::kKeys - 1)) >> 4))) & 1u));
+                    const int at = lane & (C::kKeys - 1);
+                    const uint32_t e = lds8(cur + C::kExps + at);
+                    const bool in = !edge || (key0 + at < len && !((bad >> ((i & 15) * 2 + (at >> 4))) & 1u));
                     e_max = (int)__reduce_max_sync(0xffffffffu, in ? e : 0u);
                     const int e_min = (int)__reduce_min_sync(0xffffffffu, in ? e : 255u);
                     tame = tame && e_min >= 127 - 40 && e_max <= 127 + 40;
                     near = tame && e_max - e_min <= 8;
                     e_max -= 127;
-#pragma unroll
-                    for (int x = 0; x < H; ++x)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t b8 = lds8(cur + C::kExps + x * 16 + 8 * k + g);
-                            if (edge && !(key0 + x * 16 + 8 * k + g < len && !((bad >> ((i & 15) * 2 + x)) & 1u))) b8 = 127;
-                            kv[x][k] = near ? exp_scale(b8) : (float)((int)b8 - 127);
-                        }
                 }
-                // maxima over the turn's keys (the 8 lanes with this t), rescaling, weights
+                // exponent byte of value key g + 8k of tile x; 127 where there is no such key
+                auto value_exp = [&](int x, int k) {
+                    const uint32_t e = lds8(cur + C::kExps + x * 16 + 8 * k + g);
+                    return edge && !(key0 + x * 16 + 8 * k + g < len && !((bad >> ((i & 15) * 2 + x)) & 1u)) ? 127u : e;
+                };
+                // maxima over the turn's keys (the 8 lanes with this t)
                 float mn[NT][2], rn[NT][2];
                 bool grew = false;
 #pragma unroll
@@ -370,23 +376,39 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         top *= fac[nt][j];
-                        mn[nt][j] = fmaxf(m[nt][j], top);
-                        if (F8) {
-                            float ref = top + (float)e_max;
-                            if (!near) {
-                                ref = kNoMax;
+                        mn[nt][j] = top > m[nt][j] + kSlack ? top : m[nt][j];
+                        grew |= mn[nt][j] > m[nt][j];
+                        rn[nt][j] = top + (float)e_max;
+                    }
+                if (F8) {
+                    if (!near) {
+                        float ev[H][2];
+#pragma unroll
+                        for (int x = 0; x < H; ++x)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) ev[x][k] = (float)((int)value_exp(x, k) - 127);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float ref = kNoMax;
 #pragma unroll
                                 for (int x = 0; x < H; ++x)
 #pragma unroll
-                                    for (int k = 0; k < 2; ++k) ref = fmaxf(ref, fmaf(s[x][nt][j + 2 * k], fac[nt][j], kv[x][k]));
+                                    for (int k = 0; k < 2; ++k) ref = fmaxf(ref, fmaf(s[x][nt][j + 2 * k], fac[nt][j], ev[x][k]));
 #pragma unroll
                                 for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+                                rn[nt][j] = ref;
                             }
-                            rn[nt][j] = fmaxf(r[nt][j], ref);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            rn[nt][j] = rn[nt][j] > r[nt][j] + kSlack ? rn[nt][j] : r[nt][j];
                             grew |= rn[nt][j] > r[nt][j];
                         }
-                        grew |= mn[nt][j] > m[nt][j];
-                    }
+                }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -407,50 +429,81 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                             }
                         }
                 }
+                // weights, in place of the scores
                 uint32_t ph[H][NT][2], pl[H][NT][2];    // B fragments of P^T: hi and lo (bf16), or P' (fp16)
+                if (F8 && !near) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[H][4];
+                    for (int x = 0; x < H; ++x) {
+                        const float ev[2] = {(float)((int)value_exp(x, 0) - 127), (float)((int)value_exp(x, 1) - 127)};
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float f = F8 && near ? ex2(m[nt][j] - r[nt][j]) : 1.f;
-                        float sum = 0.f;
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float q = fmaf(s[x][nt][c], fac[nt][c & 1], -m[nt][c & 1]);
+                                s[x][nt][c] = ex2(fmaf(s[x][nt][c], fac[nt][c & 1], ev[c >> 1]) - r[nt][c & 1]);
+                                l[nt][c & 1] += ex2(q);
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float sum = 0.f;
+#pragma unroll
+                            for (int x = 0; x < H; ++x)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const float q = ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], -m[nt][j]));
+                                    sum += q;
+                                    s[x][nt][j + 2 * k] = q;
+                                }
+                            l[nt][j] += sum;
+                        }
+                    if (F8) {
+                        float kv[H][2];
 #pragma unroll
                         for (int x = 0; x < H; ++x)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float q = ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], -m[nt][j]));
-                                sum += q;
-                                w[x][j + 2 * k] = !F8 ? q
-                                                : near ? q * (f * kv[x][k])
-                                                       : ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], kv[x][k]) - r[nt][j]);
-                            }
-                        l[nt][j] += sum;
-                    }
+                            for (int k = 0; k < 2; ++k) kv[x][k] = exp_scale(value_exp(x, k));
 #pragma unroll
-                    for (int x = 0; x < H; ++x) {
-                        if (F8) {
-                            ph[x][nt][0] = movmatrix(pack_half(w[x][0], w[x][1]));
-                            ph[x][nt][1] = movmatrix(pack_half(w[x][2], w[x][3]));
-                        } else {
-                            const uint32_t h0 = bf16_pair(w[x][0], w[x][1]), h1 = bf16_pair(w[x][2], w[x][3]);
-                            ph[x][nt][0] = movmatrix(h0);
-                            ph[x][nt][1] = movmatrix(h1);
-                            pl[x][nt][0] = movmatrix(bf16_pair(w[x][0] - bf16_lo(h0), w[x][1] - bf16_hi(h0)));
-                            pl[x][nt][1] = movmatrix(bf16_pair(w[x][2] - bf16_lo(h1), w[x][3] - bf16_hi(h1)));
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float f = ex2(m[nt][j] - r[nt][j]);
+#pragma unroll
+                                for (int x = 0; x < H; ++x)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) s[x][nt][j + 2 * k] *= f * kv[x][k];
+                            }
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < H; ++x) {
+                        const float* w = s[x][nt];
+                        if (F8) {
+                            ph[x][nt][0] = movmatrix(pack_half(w[0], w[1]));
+                            ph[x][nt][1] = movmatrix(pack_half(w[2], w[3]));
+                        } else {
+                            const uint32_t h0 = bf16_pair(w[0], w[1]), h1 = bf16_pair(w[2], w[3]);
+                            ph[x][nt][0] = movmatrix(h0);
+                            ph[x][nt][1] = movmatrix(h1);
+                            pl[x][nt][0] = movmatrix(bf16_pair(w[0] - bf16_lo(h0), w[1] - bf16_hi(h0)));
+                            pl[x][nt][1] = movmatrix(bf16_pair(w[2] - bf16_lo(h1), w[3] - bf16_hi(h1)));
+                        }
+                    }
                 // O^T += V^T P^T
 #pragma unroll
                 for (int x = 0; x < H; ++x) {
-                    const uint32_t vs = cur + x * V::kBytes;
+                    const uint32_t at = cur + x * V::kBytes + value_at;
                     const int keyx = key0 + x * kTileKeys;
                     uint32_t v[V::kChunks][4][4];
 #pragma unroll
                     for (int u = 0; u < V::kChunks; ++u)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) V::load(vs, j, u, lane, v[u][j]);
+                        for (int j = 0; j < 4; ++j) V::load(at + V::load_step(j, u), v[u][j]);
                     // A row that does not see a key must not meet its values even with weight 0 (0 * inf
                     // and 0 * NaN are NaN): where such a tile holds values that are not finite, each query
                     // position is done by itself with the keys behind its limit cleared.
@@ -483,10 +536,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         if (F8) {
                             const uint32_t sel = (y & 1) ? 0x7362u : 0x5140u;
                             const uint32_t lo = __byte_perm(k0, k1, sel), hi = __byte_perm(k2, k3, sel);
-                            a[0] = e4m3x2_half2(lo);
-                            a[1] = e4m3x2_half2(lo >> 16);
-                            a[2] = e4m3x2_half2(hi);
-                            a[3] = e4m3x2_half2(hi >> 16);
+                            e4m3x4_half2(lo, a[0], a[1]);
+                            e4m3x4_half2(hi, a[2], a[3]);
                         } else {
                             a[0] = __byte_perm(k0, k1, 0x5410);
                             a[1] = __byte_perm(k0, k1, 0x7632);
@@ -562,8 +613,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         make_float2(o[mt][nt][j], o[mt][nt][j + 2]);
         }
         __syncthreads();
-        const bool whole = n == units;
-        float* part = p.part + ((size_t)blockIdx.x * 2 + (pos == g0 ? 0 : 1)) * C::kPart;
+        const bool whole = walk.complete();
+        float* part = p.part + (size_t)walk.slot() * C::kPart;
         const int rows = min(C::kRows, p.rows - row0);
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kPagedThreads) {
             const int i = idx / (D / 4), c = idx % (D / 4);
@@ -593,87 +644,99 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
             }
         }
         __syncthreads();
-
-        pos += n;
-        if (pos < g1 && pos - base == units * p.Hkv * p.rblocks) {
-            base = pos;
-            do {
-                len = seq_len(p, ++b);
-            } while (len == 0);
-            units = (len + C::kUnit - 1) / C::kUnit;
-        }
     }
 }
 
 // Joins the partial states of the segments that were cut.  Block x looks at the boundary
 // between the shares of CTAs x and x + 1 and takes the segment that is cut there for the first
-// time; blockIdx.y and gridDim.y deal out its rows.  The four warps take every fourth state.
+// time; blockIdx.y and gridDim.y deal out its rows.  `each` warps take a row, every each-th state
+// each (in a fixed order), and meet in shared memory.
+constexpr int kJoinThreads = 256;
+constexpr int kBatch = 8;              // states a warp loads together
+
 template <int D, int NT, int UNIT>
-__global__ void __launch_bounds__(kPagedThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
-    constexpr int kRows = 8 * NT, kStride = D + 4, kPart = kRows * kStride;
-    __shared__ int red[8];
-    __shared__ float st[kPagedWarps][4];
-    __shared__ float4 ac[kPagedWarps][32];
+__global__ void __launch_bounds__(kJoinThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
+    constexpr int kRows = 8 * NT, kStride = D + 4, kPart = kRows * kStride, kWarps = kJoinThreads / 32;
+    __shared__ float st[kWarps][4];
+    __shared__ float4 ac[kWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int total = plan_total<UNIT>(p, red);
-    const int share = plan_share(p, total);
-    const long long cut = (long long)(blockIdx.x + 1) * share;
-    int b = 0, base = 0;
-    const bool in = cut < total;
-    if (in) plan_locate<UNIT>(p, (int)cut, red, b, base);
+    PagedCut<UNIT> cut;
+    const bool mine = cut.find(p, blockIdx.x);            // needs the lengths only
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!in) return;
-    const int units = seq_units<UNIT>(p, b);
-    const int seg = ((int)cut - base) / units, s0 = base + seg * units;
-    if (s0 == (int)cut || s0 / share != (int)blockIdx.x) return;   // not cut here, or cut before
-    const int c0 = s0 / share, c1 = (s0 + units - 1) / share;
-    const int h = seg / p.rblocks, rb = seg - h * p.rblocks, row0 = rb * kRows;
-    const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
-    const int rows = min(kRows, p.rows - row0);
-    const int first_slot = 2 * c0 + (s0 == c0 * share ? 0 : 1);
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    if (!mine) return;
+    const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
+    const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
+    const int rows = min(kRows, p.rows - row0), states = cut.c1 - cut.c0 + 1;
+    const int each = states <= 8 ? 1 : states <= 32 ? 4 : 8;
+    const int part = warp & (each - 1), group = warp / each, groups = kWarps / each;
+    for (int r0 = blockIdx.y * groups; r0 < rows; r0 += gridDim.y * groups) {
+        const int r = r0 + group;
         float M = kNoMax, MV = kNoMax, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0 + warp; c <= c1; c += kPagedWarps) {
-            const float* from = p.part + (size_t)(c == c0 ? first_slot : 2 * c) * kPart + r * kStride;
-            const float4 s = *reinterpret_cast<const float4*>(from + D);
-            const float4 x = lane < D / 4 ? *reinterpret_cast<const float4*>(from + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float Mn = fmaxf(M, s.x), Vn = fmaxf(MV, s.y);
-            L = L * ex2(M - Mn) + s.z * ex2(s.x - Mn);
-            const float f0 = ex2(MV - Vn), f1 = ex2(s.y - Vn);
-            acc.x = acc.x * f0 + x.x * f1;
-            acc.y = acc.y * f0 + x.y * f1;
-            acc.z = acc.z * f0 + x.z * f1;
-            acc.w = acc.w * f0 + x.w * f1;
-            M = Mn;
-            MV = Vn;
-        }
-        __syncthreads();
-        if (lane == 0) {
-            st[warp][0] = M;
-            st[warp][1] = MV;
-            st[warp][2] = L;
-        }
-        ac[warp][lane] = acc;
-        __syncthreads();
-        if (warp == 0 && lane < D / 4) {
-            M = fmaxf(fmaxf(st[0][0], st[1][0]), fmaxf(st[2][0], st[3][0]));
-            MV = fmaxf(fmaxf(st[0][1], st[1][1]), fmaxf(st[2][1], st[3][1]));
-            L = 0.f;
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            for (int c = cut.c0 + part; c <= cut.c1; c += kBatch * each) {
+                float4 q[kBatch], x[kBatch];
 #pragma unroll
-            for (int w = 0; w < kPagedWarps; ++w) {
-                const float f = ex2(st[w][0] - M), fv = ex2(st[w][1] - MV);
-                const float4 x = ac[w][lane];
-                L = fmaf(st[w][2], f, L);
-                acc.x = fmaf(x.x, fv, acc.x);
-                acc.y = fmaf(x.y, fv, acc.y);
-                acc.z = fmaf(x.z, fv, acc.z);
-                acc.w = fmaf(x.w, fv, acc.w);
+                for (int k = 0; k < kBatch; ++k) {
+                    const int ck = c + k * each;
+                    const float* from = p.part + (size_t)cut.slot(ck <= cut.c1 ? ck : c) * kPart + r * kStride;
+                    q[k] = *reinterpret_cast<const float4*>(from + D);
+                    x[k] = *reinterpret_cast<const float4*>(from + 4 * (lane % (D / 4)));
+                    if (ck > cut.c1) {
+                        q[k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+                        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+                float Mn = M, Vn = MV;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    Mn = fmaxf(Mn, q[k].x);
+                    Vn = fmaxf(Vn, q[k].y);
+                }
+                const float f0 = ex2(MV - Vn);
+                L *= ex2(M - Mn);
+                acc.x *= f0;
+                acc.y *= f0;
+                acc.z *= f0;
+                acc.w *= f0;
+                M = Mn;
+                MV = Vn;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float f1 = ex2(q[k].y - Vn);
+                    L = fmaf(q[k].z, ex2(q[k].x - Mn), L);
+                    acc.x = fmaf(x[k].x, f1, acc.x);
+                    acc.y = fmaf(x[k].y, f1, acc.y);
+                    acc.z = fmaf(x[k].z, f1, acc.z);
+                    acc.w = fmaf(x[k].w, f1, acc.w);
+                }
             }
-            attn_finish<D>(p, qrow + row0 + r, lane, acc, M, MV, L);
         }
+        if (each > 1) {
+            __syncthreads();
+            if (lane == 0) {
+                st[warp][0] = M;
+                st[warp][1] = MV;
+                st[warp][2] = L;
+            }
+            ac[warp][lane] = acc;
+            __syncthreads();
+            if (part == 0) {
+                for (int w = warp + 1; w < warp + each; ++w) {
+                    const float Mn = fmaxf(M, st[w][0]), Vn = fmaxf(MV, st[w][1]);
+                    const float4 x = ac[w][lane];
+                    L = L * ex2(M - Mn) + st[w][2] * ex2(st[w][0] - Mn);
+                    const float f0 = ex2(MV - Vn), f1 = ex2(st[w][1] - Vn);
+                    acc.x = acc.x * f0 + x.x * f1;
+                    acc.y = acc.y * f0 + x.y * f1;
+                    acc.z = acc.z * f0 + x.z * f1;
+                    acc.w = acc.w * f0 + x.w * f1;
+                    M = Mn;
+                    MV = Vn;
+                }
+            }
+        }
+        if (part == 0 && r < rows && lane < D / 4) attn_finish<D>(p, qrow + row0 + r, lane, acc, M, MV, L);
     }
 }
 

@@ -4,6 +4,7 @@
 
 namespace {
 
+constexpr int kWholeUnits = 8;
 constexpr int kPagedMaxCtas = 4;     // most resident CTAs per SM of any variant
 
 int page_shift_of(int n) {
@@ -14,6 +15,42 @@ int page_shift_of(int n) {
 
 // Blocks of 8, 16, 24 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
 int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Launches a kernel whose shared memory needs an attribute that lasts as long as the device's context.  These
+// calls are made per token, so it is set once per kernel and device (`done`, a bit per device) and
+// again where a launch fails without it (after a cudaDeviceReset).
+template <typename K>
+int launch_main(K kernel, int smem, const skl::PagedParams& p, cudaStream_t st, std::atomic<unsigned long long>& done,
+                const char* what) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    for (bool set = (done.load(std::memory_order_relaxed) & bit) == 0;; set = true) {
+        if (set) {
+            const int rc = set_smem(kernel, smem);
+            if (rc) return rc;
+            done.fetch_or(bit, std::memory_order_relaxed);
+        }
+        kernel<<<p.grid, skl::kPagedThreads, smem, st>>>(p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) return STREAMKL_OK;
+        if (set) return cuda_fail(e, what);
+    }
+}
+
+// The grid, and whether segments are dealt out whole: where no segment has more than kWholeUnits units.
+// (One sequence of 300 keys, 8 KV heads, d = 128: FIGURE.)
+template <int UNIT>
+void paged_grid(skl::PagedParams* p, int ctas) {
+    const long long units = ((long long)p->width * p->page_size + UNIT - 1) / UNIT;
+    const long long segments = (long long)p->B * p->Hkv * p->rblocks;
+    p->grid = ctas * num_sms();
+    p->whole = units <= kWholeUnits ? 1 : 0;
+    if (p->whole) p->grid = (int)std::min<long long>(p->grid, segments);
+}
 
 int check_cache(const streamkl_cache* c, bool values) {
     if (!c || !c->k || (values && !c->v)) return STREAMKL_ERR_INVALID_ARG;
@@ -99,17 +136,16 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     p->page_size = c->page_size;
     p->page_shift = page_shift_of(c->page_size);
     p->causal = causal ? 1 : 0;
-    p->min_units = 1;
     p->sl2 = scale * 1.4426950408889634f;
     p->part = static_cast<float*>(workspace);
     return STREAMKL_OK;
 }
 
 template <typename K>
-int launch_join(K kernel, const skl::PagedParams& p, int gy, cudaStream_t st, const char* what) {
+int launch_join(K kernel, int threads, const skl::PagedParams& p, int gy, cudaStream_t st, const char* what) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
-    cfg.blockDim = dim3(skl::kPagedThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -125,17 +161,14 @@ template <int D, bool F8, int NT>
 int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     using C = skl::AttnCfg<D, F8, NT>;
     static_assert(C::kCtas <= kPagedMaxCtas, "workspace");
-    p.grid = C::kCtas * num_sms();
-    auto kern = skl::streamkl_paged_attn_kernel<D, F8, NT>;
-    int rc = set_smem(kern, C::kSmem);
-    if (rc) return rc;
-    kern<<<p.grid, skl::kPagedThreads, C::kSmem, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_attn launch");
+    static std::atomic<unsigned long long> done{0};
+    paged_grid<C::kUnit>(&p, C::kCtas);
+    const int rc = launch_main(skl::streamkl_paged_attn_kernel<D, F8, NT>, C::kSmem, p, st, done, "streamkl_paged_attn launch");
+    if (rc || p.whole) return rc;
     // few segments: each has many partial states, and its rows go to CTAs of their own
     const long long segments = (long long)p.B * p.Hkv * p.rblocks;
-    const int gy = segments * 4 <= p.grid ? std::min(p.rows, 8 * NT) : 1;
-    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, p, gy, st, "streamkl_paged_attn join launch");
+    const int gy = segments * 16 <= p.grid ? std::min(p.rows, 8 * NT) : NT;
+    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, skl::kJoinThreads, p, gy, st, "streamkl_paged_attn join launch");
 }
 
 template <int D, bool F8>
@@ -151,14 +184,12 @@ int launch_paged_attn_rows(const skl::PagedParams& p, cudaStream_t st) {
 template <int D, bool F1, bool F2, bool SHARED, int NT>
 int launch_paged_kl(skl::PagedParams p, cudaStream_t st) {
     using C = skl::KlCfg<D, F1, F2, SHARED, NT>;
-    p.grid = 2 * num_sms();
-    auto kern = skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>;
-    int rc = set_smem(kern, C::kSmem);
-    if (rc) return rc;
-    kern<<<p.grid, skl::kPagedThreads, C::kSmem, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_kl launch");
-    return launch_join(skl::streamkl_paged_kl_join_kernel<NT, C::kUnit>, p, 1, st, "streamkl_paged_kl join launch");
+    static_assert(C::kCtas <= kPagedMaxCtas, "workspace");
+    static std::atomic<unsigned long long> done{0};
+    paged_grid<C::kUnit>(&p, C::kCtas);
+    const int rc = launch_main(skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>, C::kSmem, p, st, done, "streamkl_paged_kl launch");
+    if (rc || p.whole) return rc;
+    return launch_join(skl::streamkl_paged_kl_join_kernel<NT, C::kUnit>, skl::kPagedThreads, p, 1, st, "streamkl_paged_kl join launch");
 }
 
 template <int D, bool F1, bool F2, bool SHARED>
@@ -204,7 +235,7 @@ int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const in
     if (!q || !out || !lse) return STREAMKL_ERR_INVALID_ARG;
     int rc = check_cache(cache, true);
     if (rc) return rc;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(lse)) return STREAMKL_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(lse)) return STREAMKL_ERR_UNSUPPORTED;
     skl::PagedParams p = {};
     if ((rc = paged_params(cache, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
         return rc;
@@ -232,9 +263,8 @@ int streamkl_paged_kl(const streamkl_cache* cache1, const uint16_t* q1, const st
         return STREAMKL_ERR_UNSUPPORTED;
     const bool shared = cache1->k == cache2->k;
     if (shared && (cache1->type != cache2->type || cache1->k_exp != cache2->k_exp)) return STREAMKL_ERR_INVALID_ARG;
-    const void* ptrs[] = {q1, q2, kl, lse1, lse2};
-    for (const void* ptr : ptrs)
-        if (!aligned16(ptr)) return STREAMKL_ERR_UNSUPPORTED;
+    if (!aligned16(q1) || !aligned16(q2) || !aligned4(kl) || !aligned4(lse1) || !aligned4(lse2))
+        return STREAMKL_ERR_UNSUPPORTED;
     skl::PagedParams p = {};
     if ((rc = paged_params(cache1, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
         return rc;

@@ -29,19 +29,19 @@ struct KlCfg {
     static constexpr int kUnit = kPagedWarps * kTileKeys;
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
+    static constexpr int kCtas = NT == 1 ? 3 : 2;                          // on an SM
     static constexpr int kOff2 = K1::kBytes;
     static constexpr int kExp1 = kOff2 + (SHARED ? 0 : K2::kBytes);
     static constexpr int kExp2 = kExp1 + (F1 ? 16 : 0);
-    static constexpr int kStage = kExp2 + (F2 && !SHARED ? 16 : 0);
-    static constexpr int kMax = 24 * 1024 / kStage;
+    static constexpr int kStage = (kExp2 + (F2 && !SHARED ? 16 : 0) + 127) / 128 * 128;
+    static constexpr int kMax = (kCtas == 3 ? 18 : 26) * 1024 / kStage;
     static constexpr int kStages = kMax > 8 ? 8 : kMax;
     static constexpr int kWarp = kStage * kStages;
     static constexpr bool kSharedQ = NT > 2;
     static constexpr int kQ = kPagedWarps * kWarp;                         // [2][NT][steps][lane]
     static constexpr int kFactor = kQ + (kSharedQ ? 2 * NT * kSteps * 32 * 8 : 0);   // [2][NT][8]
     static constexpr int kStats = kFactor + (kSharedQ ? 2 * NT * 8 * 4 : 0);         // [warp][5][kRows]
-    static constexpr int kRed = kStats + kPagedWarps * 5 * kRows * 4;
-    static constexpr int kSmem = kRed + 64;
+    static constexpr int kSmem = kStats + kPagedWarps * 5 * kRows * 4;
     static constexpr int kPart = kRows * 5;
 };
 
@@ -70,23 +70,21 @@ __device__ __forceinline__ void kl_finish(const PagedParams& p, size_t row, cons
     p.kl[row] = (float)(ln2 * ((double)a[4] / (double)a[1] + ((double)a[2] - (double)a[0]) + (g2 - g1)));
 }
 
-// S^T of one tile: c[nt] += K Q^T for every block of 8 query rows.
+// S^T of one tile: c[nt] += K Q^T for every block of 8 query rows.  at: the lane's load offsets.
 template <int D, bool F8, int NT, bool SHARED_Q>
-__device__ __forceinline__ void tile_scores(uint32_t ks, int lane, const uint2* qf, uint32_t qs, float (*c)[4]) {
+__device__ __forceinline__ void tile_scores(uint32_t ks, const uint32_t* at, int lane, const uint2* qf, uint32_t qs, float (*c)[4]) {
     using K = KeyTile<D, F8>;
     constexpr int kSteps = D / 16;
 #pragma unroll
     for (int u = 0; u < K::kChunks; ++u) {
-        const uint4 x = K::load(ks, 0, u, lane), y = K::load(ks, 1, u, lane);
+        const uint4 x = lds128(ks + at[u & 1] + K::load_step(0, u)), y = lds128(ks + at[u & 1] + K::load_step(1, u));
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int w = 0; w < K::kSteps; ++w) {
             uint32_t a0, a1, a2, a3;
             if (F8) {
-                a0 = e4m3x2_half2(xw[w]);
-                a1 = e4m3x2_half2(yw[w]);
-                a2 = e4m3x2_half2(xw[w] >> 16);
-                a3 = e4m3x2_half2(yw[w] >> 16);
+                e4m3x4_half2(xw[w], a0, a2);
+                e4m3x4_half2(yw[w], a1, a3);
             } else {
                 a0 = xw[(2 * w) & 3];
                 a1 = yw[(2 * w) & 3];
@@ -105,16 +103,19 @@ __device__ __forceinline__ void tile_scores(uint32_t ks, int lane, const uint2* 
 }
 
 template <int D, bool F1, bool F2, bool SHARED, int NT>
-__global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::kCtas) streamkl_paged_kl_kernel(const PagedParams p) {
     using C = KlCfg<D, F1, F2, SHARED, NT>;
     using K1 = typename C::K1;
     using K2 = typename C::K2;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
-    const uint32_t stage0 = sb + warp * C::kWarp;
+    const uint32_t ring = sb + warp * C::kWarp;
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
-    int* red = reinterpret_cast<int*>(smem + C::kRed);
+    // where this lane copies to and loads from in every tile
+    const uint32_t to1 = K1::copy_offset(lane), to2 = K2::copy_offset(lane);
+    const uint32_t at1[2] = {(uint32_t)K1::load_offset(lane, 0), (uint32_t)K1::load_offset(lane, K1::kChunks > 1)};
+    const uint32_t at2[2] = {(uint32_t)K2::load_offset(lane, 0), (uint32_t)K2::load_offset(lane, K2::kChunks > 1)};
 
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (threadIdx.x == 0 && (p.lengths[b] < 0 || p.lengths[b] > p.width * p.page_size)) g_page_status = 5;
@@ -126,50 +127,42 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
         }
     }
 
-    const int total = plan_total<C::kUnit>(p, red);
-    const int share = plan_share(p, total);
-    const long long first = (long long)blockIdx.x * share;
-    if (first >= total) return;
-    const int g0 = (int)first, g1 = (int)min((long long)total, first + share);
-    int b, base;
-    plan_locate<C::kUnit>(p, g0, red, b, base);
-    int len = seq_len(p, b), units = (len + C::kUnit - 1) / C::kUnit;
-
-    for (int pos = g0; pos < g1;) {
-        const int off = pos - base, seg = off / units, u0 = off - seg * units;
-        const int n = min(units - u0, g1 - pos);
-        const int h = seg / p.rblocks, rb = seg - h * p.rblocks;
+    PagedWalk<C::kUnit> walk;
+    for (bool more = walk.start(p); more; more = walk.next(p)) {
+        const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
+        const int h = walk.seg / p.rblocks, rb = walk.seg - h * p.rblocks;
         const int row0 = rb * C::kRows;
-        const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
-        const int* table = p.table + (size_t)b * p.width;
-        const int key00 = u0 * C::kUnit + warp * kTileKeys;
-        uint32_t bad = 0;
-
-        auto issue = [&](int i, int s) {
-            const int key0 = key00 + i * C::kUnit;
-            const uint32_t dst = stage0 + s * C::kStage;
-            bad &= ~(1u << s);
-            if (key0 < len) {
-                const int page = __ldg(table + (key0 >> p.page_shift));
-                if ((unsigned)page < (unsigned)p.pages) {
-                    const size_t row = ((size_t)page * p.Hkv + h) * p.page_size + (key0 & (p.page_size - 1));
-                    const int valid = len - key0;
-                    K1::copy(dst, p.a.rows + row * K1::kRow, valid, lane);
-                    if (!SHARED) K2::copy(dst + C::kOff2, p.b.rows + row * K2::kRow, valid, lane);
-                    if (F1 && lane == 0) cp_async16(dst + C::kExp1, p.a.exps + row, 16);
-                    if (F2 && !SHARED && lane == 1) cp_async16(dst + C::kExp2, p.b.exps + row, 16);
-                } else {
-                    bad |= 1u << s;
+        const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
+        const int* table = p.table + (size_t)walk.b * p.width;
+        const int key00 = walk.u0 * C::kUnit + warp * kTileKeys;
+        int page;                 // of the tile that is requested next
+        uint32_t bad = 0;         // bit (turn % 32): no such page
+        auto look_up = [&](int i) {
+            const int key = key00 + i * C::kUnit;
+            page = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
+        };
+        auto request = [&](int i, uint32_t dst) {
+            if (i < n) {
+                const int key = key00 + i * C::kUnit;
+                const bool there = (unsigned)page < (unsigned)p.pages;
+                const int valid = there ? len - key : 0;
+                const int row = there && key < len ? (page * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
+                bad &= ~(1u << (i & 31));
+                if (!there) {
+                    bad |= 1u << (i & 31);
                     if (lane == 0) g_page_status = 5;
                 }
+                K1::copy(dst + to1, p.a.rows + lane * 16 + (size_t)row * K1::kRow, valid, lane);
+                if (!SHARED) K2::copy(dst + C::kOff2 + to2, p.b.rows + lane * 16 + (size_t)row * K2::kRow, valid, lane);
+                if (F1 && lane == 0) cp_async16(dst + C::kExp1, p.a.exps + row, 16);
+                if (F2 && !SHARED && lane == 1) cp_async16(dst + C::kExp2, p.b.exps + row, 16);
+                look_up(i + 1);
             }
             cp_commit();
         };
+        look_up(0);
 #pragma unroll
-        for (int s = 0; s < C::kStages - 1; ++s) {
-            if (s < n) issue(s, s);
-            else cp_commit();
-        }
+        for (int i = 0; i < C::kStages - 1; ++i) request(i, ring + i * C::kStage);
 
         uint2 qf1[C::kSharedQ ? 1 : NT * C::kSteps], qf2[C::kSharedQ ? 1 : NT * C::kSteps];
         float fac1[NT][2], fac2[NT][2];
@@ -210,36 +203,37 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
                 fac2[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }
         }
-        int lim[NT][2];
+        // first key that a row does not see (of query 2t + j of block nt); the least over all rows
+        auto limit = [&](int nt, int j) {
+            return p.causal ? len - (p.NQ - 1) + (row0 + nt * 8 + 2 * t + j) % p.NQ : len;
+        };
         float a[NT][2][5];      // m1, l1, m2, l2, acc of this lane's keys
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                lim[nt][j] = p.causal ? len - (p.NQ - 1) + (row0 + nt * 8 + 2 * t + j) % p.NQ : len;
                 a[nt][j][0] = a[nt][j][2] = kNoMax;
                 a[nt][j][1] = a[nt][j][3] = a[nt][j][4] = 0.f;
             }
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        int st = 0;
-        for (int i = 0; i < n; ++i, st = st + 1 == C::kStages ? 0 : st + 1) {
-            __syncwarp();
-            if (i + C::kStages - 1 < n) issue(i + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
-            else cp_commit();
+        uint32_t ks = ring, last = ring + (C::kStages - 1) * C::kStage;     // stages of this turn and the one before
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, last = ks, ks = ks == ring + (C::kStages - 1) * C::kStage ? ring : ks + C::kStage) {
+            __syncwarp();       // every lane is done with the stage that is refilled
+            request(i + C::kStages - 1, last);
             cp_wait<C::kStages - 1>();
-            __syncwarp();
+            __syncwarp();       // what other lanes copied
             const int key0 = key00 + i * C::kUnit;
-            if (key0 >= len || ((bad >> st) & 1u)) continue;
-            const uint32_t ks = stage0 + st * C::kStage;
+            if (key0 >= len || ((bad >> (i & 31)) & 1u)) continue;
 
             float s1[NT][4], s2[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) s1[nt][c] = s2[nt][c] = 0.f;
-            tile_scores<D, F1, NT, C::kSharedQ>(ks, lane, qf1, sb + C::kQ, s1);
-            tile_scores<D, F2, NT, C::kSharedQ>(SHARED ? ks : ks + C::kOff2, lane, qf2, sb + C::kQ + NT * C::kSteps * 256, s2);
+            tile_scores<D, F1, NT, C::kSharedQ>(ks, at1, lane, qf1, sb + C::kQ, s1);
+            tile_scores<D, F2, NT, C::kSharedQ>(SHARED ? ks : ks + C::kOff2, at2, lane, qf2, sb + C::kQ + NT * C::kSteps * 256, s2);
             float k1[2] = {1.f, 1.f}, k2[2] = {1.f, 1.f};
             if (F1) {
                 k1[0] = exp_scale(lds8(ks + C::kExp1 + g));
@@ -250,32 +244,66 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
                 k2[1] = SHARED ? k1[1] : exp_scale(lds8(ks + C::kExp2 + 8 + g));
             }
             const bool edge = key0 + kTileKeys > least;
+            // scores in base 2, their difference, and whether a lane's references have to move
+            float u[NT][2][2], v[NT][2][2], d[NT][2][2];
+            bool grew = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float u[2], v[2], d[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        u[k] = s1[nt][j + 2 * k] * fac1[nt][j];
-                        v[k] = s2[nt][j + 2 * k] * fac2[nt][j];
-                        if (F1) u[k] *= k1[k];
-                        if (F2) v[k] *= k2[k];
-                        d[k] = u[k] - v[k];
-                        if (edge && key0 + g + 8 * k >= lim[nt][j]) {
-                            u[k] = v[k] = -INFINITY;
-                            d[k] = 0.f;
-                        }
+                        float x = s1[nt][j + 2 * k] * fac1[nt][j], y = s2[nt][j + 2 * k] * fac2[nt][j];
+                        if (F1) x *= k1[k];
+                        if (F2) y *= k2[k];
+                        d[nt][j][k] = x - y;
+                        u[nt][j][k] = x;
+                        v[nt][j][k] = y;
                     }
+                }
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (key0 + g + 8 * k >= limit(nt, j)) {
+                                u[nt][j][k] = v[nt][j][k] = -INFINITY;
+                                d[nt][j][k] = 0.f;
+                            }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    grew |= fmaxf(u[nt][j][0], u[nt][j][1]) > a[nt][j][0] + kSlack;
+                    grew |= fmaxf(v[nt][j][0], v[nt][j][1]) > a[nt][j][2] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float* x = a[nt][j];
+                        const float n1 = fmaxf(x[0], fmaxf(u[nt][j][0], u[nt][j][1])), n2 = fmaxf(x[2], fmaxf(v[nt][j][0], v[nt][j][1]));
+                        const float r1 = ex2(x[0] - n1);
+                        x[1] *= r1;
+                        x[4] *= r1;
+                        x[3] *= ex2(x[2] - n2);
+                        x[0] = n1;
+                        x[2] = n2;
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     float* x = a[nt][j];
-                    const float n1 = fmaxf(x[0], fmaxf(u[0], u[1])), n2 = fmaxf(x[2], fmaxf(v[0], v[1]));
-                    const float r1 = ex2(x[0] - n1), r2 = ex2(x[2] - n2);
-                    const float e0 = ex2(u[0] - n1), e1 = ex2(u[1] - n1);
-                    x[1] = fmaf(x[1], r1, e0 + e1);
-                    x[4] = fmaf(x[4], r1, fmaf(e0, d[0], e1 * d[1]));
-                    x[3] = fmaf(x[3], r2, ex2(v[0] - n2) + ex2(v[1] - n2));
-                    x[0] = n1;
-                    x[2] = n2;
+                    const float e0 = ex2(u[nt][j][0] - x[0]), e1 = ex2(u[nt][j][1] - x[0]);
+                    x[1] += e0 + e1;
+                    x[4] = fmaf(e0, d[nt][j][0], fmaf(e1, d[nt][j][1], x[4]));
+                    x[3] += ex2(v[nt][j][0] - x[2]) + ex2(v[nt][j][1] - x[2]);
                 }
         }
         cp_wait<0>();
@@ -307,24 +335,15 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
                 for (int k = 0; k < 5; ++k) y[k] = stats[(w * 5 + k) * C::kRows + r];
                 kl_join(x, y);
             }
-            if (n == units) {
+            if (walk.complete()) {
                 kl_finish(p, qrow + row0 + r, x);
             } else {
-                float* to = p.part + ((size_t)blockIdx.x * 2 + (pos == g0 ? 0 : 1)) * C::kPart + r;
+                float* to = p.part + (size_t)walk.slot() * C::kPart + r;
 #pragma unroll
                 for (int k = 0; k < 5; ++k) to[k * C::kRows] = x[k];
             }
         }
         __syncthreads();
-
-        pos += n;
-        if (pos < g1 && pos - base == units * p.Hkv * p.rblocks) {
-            base = pos;
-            do {
-                len = seq_len(p, ++b);
-            } while (len == 0);
-            units = (len + C::kUnit - 1) / C::kUnit;
-        }
     }
 }
 
@@ -333,27 +352,17 @@ __global__ void __launch_bounds__(kPagedThreads, 2) streamkl_paged_kl_kernel(con
 template <int NT, int UNIT>
 __global__ void __launch_bounds__(kPagedThreads) streamkl_paged_kl_join_kernel(const PagedParams p) {
     constexpr int kRows = 8 * NT, kPart = kRows * 5;
-    __shared__ int red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int total = plan_total<UNIT>(p, red);
-    const int share = plan_share(p, total);
-    const long long cut = (long long)(blockIdx.x + 1) * share;
-    int b = 0, base = 0;
-    const bool in = cut < total;
-    if (in) plan_locate<UNIT>(p, (int)cut, red, b, base);
+    PagedCut<UNIT> cut;
+    const bool mine = cut.find(p, blockIdx.x);            // needs the lengths only
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!in) return;
-    const int units = seq_units<UNIT>(p, b);
-    const int seg = ((int)cut - base) / units, s0 = base + seg * units;
-    if (s0 == (int)cut || s0 / share != (int)blockIdx.x) return;
-    const int c0 = s0 / share, c1 = (s0 + units - 1) / share;
-    const int h = seg / p.rblocks, rb = seg - h * p.rblocks, row0 = rb * kRows;
-    const size_t qrow = ((size_t)b * p.Hkv + h) * p.rows;
-    const int first_slot = 2 * c0 + (s0 == c0 * share ? 0 : 1);
+    if (!mine) return;
+    const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
+    const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
     for (int r = warp; r < min(kRows, p.rows - row0); r += kPagedWarps) {
         float x[5] = {kNoMax, 0.f, kNoMax, 0.f, 0.f}, y[5];
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float* from = p.part + (size_t)(c == c0 ? first_slot : 2 * c) * kPart + r;
+        for (int c = cut.c0 + lane; c <= cut.c1; c += 32) {
+            const float* from = p.part + (size_t)cut.slot(c) * kPart + r;
 #pragma unroll
             for (int k = 0; k < 5; ++k) y[k] = from[k * kRows];
             kl_join(x, y);

@@ -220,7 +220,7 @@ int streamkl_bwd_noalloc(int mode, const uint16_t* q1, const uint16_t* k1, const
  *  - streamkl_cache is a host struct that describes device memory; the library reads it during
  *    the call only.  One page table row and one length belong to a sequence: token j lies in
  *    page table[b][j / page_size], slot j % page_size.  int32 tables, lengths, positions and
- *    counts need 4-byte alignment; every other pointer 16-byte alignment.
+ *    counts and fp32 outputs need 4-byte alignment; every other pointer 16-byte alignment.
  *  - Several sequences may share pages for reading.  A slot that one append writes twice
  *    (the same page in two rows of the table) holds a mix of both.
  *  - Entries of a table row behind the sequence's last page are never used.  A used

@@ -118,13 +118,13 @@ COMMON = [
 
 @pytest.mark.parametrize("kw,want", COMMON + [
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(lse=None), INVALID), (dict(q=FAKE + 2), UNSUPPORTED),
-    (dict(out=FAKE + 8), UNSUPPORTED), (dict(lse=FAKE + 4), UNSUPPORTED)])
+    (dict(out=FAKE + 8), UNSUPPORTED), (dict(lse=FAKE + 2), UNSUPPORTED)])
 def test_bad_attention(kw, want):
     assert attn(cache(), **kw) == want
 
 
 @pytest.mark.parametrize("kw,want", COMMON + [
-    (dict(q2=None), INVALID), (dict(kl=None), INVALID), (dict(lse2=FAKE + 4), UNSUPPORTED)])
+    (dict(q2=None), INVALID), (dict(kl=None), INVALID), (dict(lse2=FAKE + 2), UNSUPPORTED)])
 def test_bad_divergence(kw, want):
     assert kl(cache(), cache(k=2 * FAKE), **kw) == want
 
