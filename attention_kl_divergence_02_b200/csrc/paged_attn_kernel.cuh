@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     using K = typename C::K;
     using V = typename C::V;
     extern __shared__ __align__(128) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join's CTAs may come as SMs fall free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
     const uint32_t ring = sb + warp * C::kWarp;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         if (lane == 0) g_page_status = 5;
                     }
                     K::copy(dst + x * K::kBytes + key_to, keys + (size_t)row[x] * K::kRow, valid[x], lane);
-                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.a.exps + row[x], 16);
+                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.a.exps + row[x]);
                 }
                 look_up(i + 1);
             }
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 #pragma unroll
                 for (int x = 0; x < H; ++x) {
                     V::copy(dst + x * V::kBytes + value_to, values + (size_t)row[x] * V::kRow, valid[x], lane);
-                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.b.exps + row[x], 16);
+                    if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.b.exps + row[x]);
                 }
             }
             cp_commit();
@@ -247,7 +248,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
         // m: reference of the sum, within kSlack of the scores' maximum; r: of the weights (bf16: m); l: sum
-        float o[D / 16][NT][4], m[NT][2], r[NT][2], l[NT][2];
+        // mr: 2^(m - r)
+        float o[D / 16][NT][4], m[NT][2], r[NT][2], mr[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 m[nt][j] = r[nt][j] = kNoMax;
+                mr[nt][j] = 1.f;
                 l[nt][j] = 0.f;
             }
         bool tame = true;       // e4m3: every value scale so far within 2^-40 .. 2^40
@@ -364,8 +367,10 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     const uint32_t e = lds8(cur + C::kExps + x * 16 + 8 * k + g);
                     return edge && !(key0 + x * 16 + 8 * k + g < len && !((bad >> ((i & 15) * 2 + x)) & 1u)) ? 127u : e;
                 };
-                // maxima over the turn's keys (the 8 lanes with this t)
-                float mn[NT][2], rn[NT][2];
+                // The lane's own maxima of the scores, and of the scores times the values' scales, against
+                // the references: only where one lies beyond them do the 8 lanes with this t exchange
+                // maxima and the sums move.
+                float lm[NT][2], lr[NT][2];
                 bool grew = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -373,12 +378,9 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     for (int j = 0; j < 2; ++j) {
                         float top = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
                         if (H == 2) top = fmaxf(top, fmaxf(s[H - 1][nt][j], s[H - 1][nt][j + 2]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        top *= fac[nt][j];
-                        mn[nt][j] = top > m[nt][j] + kSlack ? top : m[nt][j];
-                        grew |= mn[nt][j] > m[nt][j];
-                        rn[nt][j] = top + (float)e_max;
+                        lm[nt][j] = top * fac[nt][j];
+                        lr[nt][j] = lm[nt][j] + (float)e_max;
+                        grew |= lm[nt][j] > m[nt][j] + kSlack;
                     }
                 if (F8) {
                     if (!near) {
@@ -391,41 +393,44 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                float ref = kNoMax;
+                                lr[nt][j] = kNoMax;
 #pragma unroll
                                 for (int x = 0; x < H; ++x)
 #pragma unroll
-                                    for (int k = 0; k < 2; ++k) ref = fmaxf(ref, fmaf(s[x][nt][j + 2 * k], fac[nt][j], ev[x][k]));
-#pragma unroll
-                                for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-                                rn[nt][j] = ref;
+                                    for (int k = 0; k < 2; ++k)
+                                        lr[nt][j] = fmaxf(lr[nt][j], fmaf(s[x][nt][j + 2 * k], fac[nt][j], ev[x][k]));
                             }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            rn[nt][j] = rn[nt][j] > r[nt][j] + kSlack ? rn[nt][j] : r[nt][j];
-                            grew |= rn[nt][j] > r[nt][j];
-                        }
+                        for (int j = 0; j < 2; ++j) grew |= lr[nt][j] > r[nt][j] + kSlack;
                 }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float a = ex2(m[nt][j] - mn[nt][j]);
+                            float top = lm[nt][j], ref = lr[nt][j];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) {
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                                if (F8) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+                            }
+                            top = fmaxf(m[nt][j], top);
+                            float a = ex2(m[nt][j] - top);
                             l[nt][j] *= a;
-                            m[nt][j] = mn[nt][j];
-                            float av = a;
+                            m[nt][j] = top;
                             if (F8) {
-                                av = ex2(r[nt][j] - rn[nt][j]);
-                                r[nt][j] = rn[nt][j];
+                                ref = fmaxf(r[nt][j], ref);
+                                a = ex2(r[nt][j] - ref);
+                                r[nt][j] = ref;
+                                mr[nt][j] = ex2(top - ref);
                             }
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
-                                o[k][nt][j] *= av;
-                                o[k][nt][j + 2] *= av;
+                                o[k][nt][j] *= a;
+                                o[k][nt][j + 2] *= a;
                             }
                         }
                 }
@@ -470,11 +475,10 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float f = ex2(m[nt][j] - r[nt][j]);
 #pragma unroll
                                 for (int x = 0; x < H; ++x)
 #pragma unroll
-                                    for (int k = 0; k < 2; ++k) s[x][nt][j + 2 * k] *= f * kv[x][k];
+                                    for (int k = 0; k < 2; ++k) s[x][nt][j + 2 * k] *= mr[nt][j] * kv[x][k];
                             }
                     }
                 }

@@ -21,21 +21,26 @@
 
 namespace skl {
 
-// F1, F2: e4m3 (else bf16) keys of either cache; SHARED: one cache (F1 == F2).
+// F1, F2: e4m3 (else bf16) keys of either cache; SHARED: one cache (F1 == F2).  A warp folds H 16-key
+// tiles of either cache at a time: two where three stages of them fit its share of shared memory.
 template <int D, bool F1, bool F2, bool SHARED, int NT>
 struct KlCfg {
     using K1 = KeyTile<D, F1>;
     using K2 = KeyTile<D, F2>;
-    static constexpr int kUnit = kPagedWarps * kTileKeys;
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
     static constexpr int kCtas = NT == 1 ? 3 : 2;                          // on an SM
-    static constexpr int kOff2 = K1::kBytes;
-    static constexpr int kExp1 = kOff2 + (SHARED ? 0 : K2::kBytes);
-    static constexpr int kExp2 = kExp1 + (F1 ? 16 : 0);
-    static constexpr int kStage = (kExp2 + (F2 && !SHARED ? 16 : 0) + 127) / 128 * 128;
-    static constexpr int kMax = (kCtas == 3 ? 18 : 26) * 1024 / kStage;
-    static constexpr int kStages = kMax > 8 ? 8 : kMax;
+    static constexpr int kShare = (kCtas == 3 ? 18 : 26) * 1024;           // of a warp
+    static constexpr int kTiles = K1::kBytes + (SHARED ? 0 : K2::kBytes);  // one tile of each cache
+    static constexpr int H = NT <= 2 && kTiles <= 3072 ? 2 : 1;
+    static constexpr int kKeys = H * kTileKeys;
+    static constexpr int kUnit = kPagedWarps * kKeys;
+    static constexpr int kOff2 = H * K1::kBytes;
+    static constexpr int kExp1 = H * kTiles;
+    static constexpr int kExp2 = SHARED ? kExp1 : kExp1 + (F1 ? kKeys : 0);
+    static constexpr int kStage = (kExp2 + (F2 ? kKeys : 0) + 127) / 128 * 128;
+    static constexpr int kFit = kShare / kStage;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kWarp = kStage * kStages;
     static constexpr bool kSharedQ = NT > 2;
     static constexpr int kQ = kPagedWarps * kWarp;                         // [2][NT][steps][lane]
@@ -43,6 +48,7 @@ struct KlCfg {
     static constexpr int kStats = kFactor + (kSharedQ ? 2 * NT * 8 * 4 : 0);         // [warp][5][kRows]
     static constexpr int kSmem = kStats + kPagedWarps * 5 * kRows * 4;
     static constexpr int kPart = kRows * 5;
+    static_assert(kStages >= 2, "ring");
 };
 
 // Joins state b (of other keys) to state a: m1, l1, m2, l2, acc.
@@ -108,11 +114,14 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
     using K1 = typename C::K1;
     using K2 = typename C::K2;
     extern __shared__ __align__(128) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join's CTAs may come as SMs fall free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
     const uint32_t ring = sb + warp * C::kWarp;
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
-    // where this lane copies to and loads from in every tile
+    constexpr int H = C::H;
+    // where this lane copies from and to, and loads from, in every tile
+    const uint8_t *keys1 = p.a.rows + lane * 16, *keys2 = p.b.rows + lane * 16;
     const uint32_t to1 = K1::copy_offset(lane), to2 = K2::copy_offset(lane);
     const uint32_t at1[2] = {(uint32_t)K1::load_offset(lane, 0), (uint32_t)K1::load_offset(lane, K1::kChunks > 1)};
     const uint32_t at2[2] = {(uint32_t)K2::load_offset(lane, 0), (uint32_t)K2::load_offset(lane, K2::kChunks > 1)};
@@ -134,28 +143,34 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         const int row0 = rb * C::kRows;
         const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)walk.b * p.width;
-        const int key00 = walk.u0 * C::kUnit + warp * kTileKeys;
-        int page;                 // of the tile that is requested next
-        uint32_t bad = 0;         // bit (turn % 32): no such page
+        const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
+        int page[H];              // of the tiles that are requested next
+        uint32_t bad = 0;         // bit (turn % 16) * 2 + tile: no such page
         auto look_up = [&](int i) {
-            const int key = key00 + i * C::kUnit;
-            page = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
+#pragma unroll
+            for (int x = 0; x < H; ++x) {
+                const int key = key00 + i * C::kUnit + x * kTileKeys;
+                page[x] = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
+            }
         };
         auto request = [&](int i, uint32_t dst) {
             if (i < n) {
-                const int key = key00 + i * C::kUnit;
-                const bool there = (unsigned)page < (unsigned)p.pages;
-                const int valid = there ? len - key : 0;
-                const int row = there && key < len ? (page * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
-                bad &= ~(1u << (i & 31));
-                if (!there) {
-                    bad |= 1u << (i & 31);
-                    if (lane == 0) g_page_status = 5;
+                bad &= ~(3u << ((i & 15) * 2));
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    const int key = key00 + i * C::kUnit + x * kTileKeys;
+                    const bool there = (unsigned)page[x] < (unsigned)p.pages;
+                    const int valid = there ? len - key : 0;
+                    const int row = there && key < len ? (page[x] * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
+                    if (!there) {
+                        bad |= 1u << ((i & 15) * 2 + x);
+                        if (lane == 0) g_page_status = 5;
+                    }
+                    K1::copy(dst + x * K1::kBytes + to1, keys1 + (size_t)row * K1::kRow, valid, lane);
+                    if (!SHARED) K2::copy(dst + C::kOff2 + x * K2::kBytes + to2, keys2 + (size_t)row * K2::kRow, valid, lane);
+                    if (F1 && lane == x) cp_async16(dst + C::kExp1 + x * kTileKeys, p.a.exps + row);
+                    if (F2 && !SHARED && lane == H + x) cp_async16(dst + C::kExp2 + x * kTileKeys, p.b.exps + row);
                 }
-                K1::copy(dst + to1, p.a.rows + lane * 16 + (size_t)row * K1::kRow, valid, lane);
-                if (!SHARED) K2::copy(dst + C::kOff2 + to2, p.b.rows + lane * 16 + (size_t)row * K2::kRow, valid, lane);
-                if (F1 && lane == 0) cp_async16(dst + C::kExp1, p.a.exps + row, 16);
-                if (F2 && !SHARED && lane == 1) cp_async16(dst + C::kExp2, p.b.exps + row, 16);
                 look_up(i + 1);
             }
             cp_commit();
@@ -225,60 +240,69 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
             cp_wait<C::kStages - 1>();
             __syncwarp();       // what other lanes copied
             const int key0 = key00 + i * C::kUnit;
-            if (key0 >= len || ((bad >> (i & 31)) & 1u)) continue;
+            if (key0 >= len) continue;
 
-            float s1[NT][4], s2[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s1[nt][c] = s2[nt][c] = 0.f;
-            tile_scores<D, F1, NT, C::kSharedQ>(ks, at1, lane, qf1, sb + C::kQ, s1);
-            tile_scores<D, F2, NT, C::kSharedQ>(SHARED ? ks : ks + C::kOff2, at2, lane, qf2, sb + C::kQ + NT * C::kSteps * 256, s2);
-            float k1[2] = {1.f, 1.f}, k2[2] = {1.f, 1.f};
-            if (F1) {
-                k1[0] = exp_scale(lds8(ks + C::kExp1 + g));
-                k1[1] = exp_scale(lds8(ks + C::kExp1 + 8 + g));
-            }
-            if (F2) {
-                k2[0] = SHARED ? k1[0] : exp_scale(lds8(ks + C::kExp2 + g));
-                k2[1] = SHARED ? k1[1] : exp_scale(lds8(ks + C::kExp2 + 8 + g));
-            }
-            const bool edge = key0 + kTileKeys > least;
             // scores in base 2, their difference, and whether a lane's references have to move
-            float u[NT][2][2], v[NT][2][2], d[NT][2][2];
+            float u[H][NT][2][2], v[H][NT][2][2], d[H][NT][2][2];
             bool grew = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < H; ++x) {
+                float s1[NT][4], s2[NT][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x = s1[nt][j + 2 * k] * fac1[nt][j], y = s2[nt][j + 2 * k] * fac2[nt][j];
-                        if (F1) x *= k1[k];
-                        if (F2) y *= k2[k];
-                        d[nt][j][k] = x - y;
-                        u[nt][j][k] = x;
-                        v[nt][j][k] = y;
-                    }
+                    for (int c = 0; c < 4; ++c) s1[nt][c] = s2[nt][c] = 0.f;
+                tile_scores<D, F1, NT, C::kSharedQ>(ks + x * K1::kBytes, at1, lane, qf1, sb + C::kQ, s1);
+                tile_scores<D, F2, NT, C::kSharedQ>(SHARED ? ks + x * K1::kBytes : ks + C::kOff2 + x * K2::kBytes, at2, lane, qf2,
+                                                    sb + C::kQ + NT * C::kSteps * 256, s2);
+                float k1[2] = {1.f, 1.f}, k2[2] = {1.f, 1.f};
+                if (F1) {
+                    k1[0] = exp_scale(lds8(ks + C::kExp1 + x * 16 + g));
+                    k1[1] = exp_scale(lds8(ks + C::kExp1 + x * 16 + 8 + g));
                 }
-            if (edge) {
+                if (F2) {
+                    k2[0] = SHARED ? k1[0] : exp_scale(lds8(ks + C::kExp2 + x * 16 + g));
+                    k2[1] = SHARED ? k1[1] : exp_scale(lds8(ks + C::kExp2 + x * 16 + 8 + g));
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (key0 + g + 8 * k >= limit(nt, j)) {
-                                u[nt][j][k] = v[nt][j][k] = -INFINITY;
-                                d[nt][j][k] = 0.f;
-                            }
+                        for (int k = 0; k < 2; ++k) {
+                            float y = s1[nt][j + 2 * k] * fac1[nt][j], z = s2[nt][j + 2 * k] * fac2[nt][j];
+                            if (F1) y *= k1[k];
+                            if (F2) z *= k2[k];
+                            u[x][nt][j][k] = y;
+                            v[x][nt][j][k] = z;
+                            d[x][nt][j][k] = y - z;
+                        }
+            }
+            if (key0 + C::kKeys > least || ((bad >> ((i & 15) * 2)) & 3u)) {
+#pragma unroll
+                for (int x = 0; x < H; ++x)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if (key0 + x * kTileKeys + g + 8 * k >= limit(nt, j) || ((bad >> ((i & 15) * 2 + x)) & 1u)) {
+                                    u[x][nt][j][k] = v[x][nt][j][k] = -INFINITY;
+                                    d[x][nt][j][k] = 0.f;
+                                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    grew |= fmaxf(u[nt][j][0], u[nt][j][1]) > a[nt][j][0] + kSlack;
-                    grew |= fmaxf(v[nt][j][0], v[nt][j][1]) > a[nt][j][2] + kSlack;
+                    float n1 = fmaxf(u[0][nt][j][0], u[0][nt][j][1]), n2 = fmaxf(v[0][nt][j][0], v[0][nt][j][1]);
+                    if (H == 2) {
+                        n1 = fmaxf(n1, fmaxf(u[H - 1][nt][j][0], u[H - 1][nt][j][1]));
+                        n2 = fmaxf(n2, fmaxf(v[H - 1][nt][j][0], v[H - 1][nt][j][1]));
+                    }
+                    grew |= n1 > a[nt][j][0] + kSlack;
+                    grew |= n2 > a[nt][j][2] + kSlack;
                 }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -286,7 +310,12 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float* x = a[nt][j];
-                        const float n1 = fmaxf(x[0], fmaxf(u[nt][j][0], u[nt][j][1])), n2 = fmaxf(x[2], fmaxf(v[nt][j][0], v[nt][j][1]));
+                        float n1 = x[0], n2 = x[2];
+#pragma unroll
+                        for (int y = 0; y < H; ++y) {
+                            n1 = fmaxf(n1, fmaxf(u[y][nt][j][0], u[y][nt][j][1]));
+                            n2 = fmaxf(n2, fmaxf(v[y][nt][j][0], v[y][nt][j][1]));
+                        }
                         const float r1 = ex2(x[0] - n1);
                         x[1] *= r1;
                         x[4] *= r1;
@@ -300,10 +329,13 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float* x = a[nt][j];
-                    const float e0 = ex2(u[nt][j][0] - x[0]), e1 = ex2(u[nt][j][1] - x[0]);
-                    x[1] += e0 + e1;
-                    x[4] = fmaf(e0, d[nt][j][0], fmaf(e1, d[nt][j][1], x[4]));
-                    x[3] += ex2(v[nt][j][0] - x[2]) + ex2(v[nt][j][1] - x[2]);
+#pragma unroll
+                    for (int y = 0; y < H; ++y) {
+                        const float e0 = ex2(u[y][nt][j][0] - x[0]), e1 = ex2(u[y][nt][j][1] - x[0]);
+                        x[1] += e0 + e1;
+                        x[4] = fmaf(e0, d[y][nt][j][0], fmaf(e1, d[y][nt][j][1], x[4]));
+                        x[3] += ex2(v[y][nt][j][0] - x[2]) + ex2(v[y][nt][j][1] - x[2]);
+                    }
                 }
         }
         cp_wait<0>();
