@@ -481,15 +481,26 @@ class PagedCache:
         return cls(rows[0], rows[1] if values else None, exps[0], exps[1] if values else None)
 
 
+PAGED_COUNTER_BYTES = 4096     # STREAMKL_PAGED_COUNTER_BYTES of the header
+
+
+def _new_workspace(nbytes, device):
+    import torch
+    workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=device)
+    workspace[:PAGED_COUNTER_BYTES // 4].zero_()
+    return workspace
+
+
 def paged_workspace(B, Hq, Hkv, NQ, d, device="cuda"):
-    """A workspace for paged_attn and paged_kl of these sizes, to be kept between calls."""
+    """A workspace for paged_attn and paged_kl of these sizes (or smaller ones), to be kept between calls: its
+    first PAGED_COUNTER_BYTES are zero, and every call leaves them so."""
     import torch
     device = torch.device(device)
     with torch.cuda.device(device):
         nbytes = streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d)
     if nbytes == 0:
         raise ValueError("unsupported sizes: B %d, Hq %d, Hkv %d, NQ %d, d %d" % (B, Hq, Hkv, NQ, d))
-    return torch.empty(nbytes // 4, dtype=torch.float32, device=device)
+    return _new_workspace(nbytes, device)
 
 
 def _enter(cache, stream):
@@ -604,7 +615,7 @@ def _scratch(workspace, shape, cache):
     if workspace is None:
         B, Hq, NQ, d = shape
         nbytes = streamkl_paged_workspace_bytes(B, Hq, cache.shape[1], NQ, d)
-        return _torch.empty(nbytes // 4, dtype=_torch.float32, device=cache.device), nbytes
+        return _new_workspace(nbytes, cache.device), nbytes
     if workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % (cache.device,))
     return workspace, workspace.numel() * workspace.element_size()

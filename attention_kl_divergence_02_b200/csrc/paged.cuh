@@ -10,8 +10,8 @@
 // into units (of 64 or 128 keys).  All segments' units in a row, T of them, are dealt out in equal contiguous
 // shares of P = ceil(T / grid): lengths are read on the device, so a ragged batch loads every
 // SM alike and the host needs no lengths.  A share may begin or end inside a segment; such a
-// CTA stores a partial state, and a second kernel joins the partial states of a segment in
-// the order of its CTAs (no atomics: the same inputs give the same bits).  A CTA has at most two
+// CTA stores a partial state, and the CTA that comes last joins the segment's states in the
+// order of their CTAs (whichever comes last: the same inputs give the same bits).  A CTA has at most two
 // partial segments, its first (slot 2c) and its last (slot 2c + 1), so the workspace depends on
 // the grid alone and not on the lengths.  Where the page table is so narrow that every segment is short,
 // segments are dealt out whole, and there is nothing to join.
@@ -58,6 +58,7 @@ struct PagedParams {
     float* lse1;
     float* lse2;           // divergence
     float* kl;
+    unsigned* arrived;     // [CTAs]: partial states of the segment first cut behind a CTA; all 0 between calls
     float* part;           // partial states, slot-major
 };
 
@@ -74,11 +75,12 @@ __device__ __forceinline__ int seq_units(const PagedParams& p, int b) {
 }
 
 // T: units of all segments.  Each warp computes it by itself, as the rest of the plan: 32 sequences at a
-// time, without a barrier.
+// time, without a barrier.  head: units of sequence `lane`, which most batches need not read again.
 template <int UNIT>
-__device__ __forceinline__ int plan_total(const PagedParams& p) {
-    int n = 0;
-    for (int b = threadIdx.x & 31; b < p.B; b += 32) n += seq_units<UNIT>(p, b);
+__device__ __forceinline__ int plan_total(const PagedParams& p, int& head) {
+    const int lane = threadIdx.x & 31;
+    int n = head = lane < p.B ? seq_units<UNIT>(p, lane) : 0;
+    for (int b = lane + 32; b < p.B; b += 32) n += seq_units<UNIT>(p, b);
     return __reduce_add_sync(0xffffffffu, n) * p.Hkv * p.rblocks;
 }
 
@@ -89,11 +91,11 @@ __device__ __forceinline__ int plan_share(const PagedParams& p, int total) {
 
 // The sequence that holds unit g (0 <= g < T), and the first unit of that sequence.
 template <int UNIT>
-__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int& b, int& base) {
+__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int head, int& b, int& base) {
     const int lane = threadIdx.x & 31, per = p.Hkv * p.rblocks;
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int x = b0 + lane < p.B ? seq_units<UNIT>(p, b0 + lane) * per : 0;
+        const int x = (b0 == 0 ? head : b0 + lane < p.B ? seq_units<UNIT>(p, b0 + lane) : 0) * per;
         int upto = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -117,7 +119,7 @@ __device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int& b,
 template <int UNIT>
 struct PagedWalk {
     int b, len, seg, units, u0, n;     // sequence, its keys, segment in it, its units, first unit and number of them to do
-    int pos, base, end, first;
+    int pos, base, end, first, share;
 
     __device__ __forceinline__ bool start(const PagedParams& p) {
         if (p.whole) {
@@ -125,12 +127,14 @@ struct PagedWalk {
             end = p.B * p.Hkv * p.rblocks;
             return find_whole(p);
         }
-        const int total = plan_total<UNIT>(p), share = plan_share(p, total);
+        int head;
+        const int total = plan_total<UNIT>(p, head);
+        share = plan_share(p, total);
         const long long at = (long long)blockIdx.x * share;
         if (at >= total) return false;
         first = pos = (int)at;
         end = (int)min((long long)total, at + share);
-        plan_locate<UNIT>(p, pos, b, base);
+        plan_locate<UNIT>(p, pos, head, b, base);
         len = seq_len(p, b);
         units = (len + UNIT - 1) / UNIT;
         cut();
@@ -154,7 +158,15 @@ struct PagedWalk {
         return true;
     }
     __device__ __forceinline__ bool complete() const { return n == units; }
+    // Where this CTA's partial state of the segment goes, and the segment's CTAs; their states are the first's
+    // at first_slot() and the others' at 2c.
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (pos == first ? 0 : 1); }
+    __device__ __forceinline__ int c0() const { return (base + seg * units) / share; }
+    __device__ __forceinline__ int c1() const { return (base + seg * units + units - 1) / share; }
+    __device__ __forceinline__ int first_slot() const {
+        const int s0 = base + seg * units, c = s0 / share;
+        return 2 * c + (s0 == c * share ? 0 : 1);
+    }
 
 private:
     __device__ __forceinline__ void cut() {
@@ -179,17 +191,31 @@ private:
     }
 };
 
-// The segment that is cut for the first time between the shares of CTAs `block` and `block` + 1.
+// Called by all threads of a CTA once its partial state of a segment is written: true in the one that
+// comes last of `states`, which then may read them all (past L1, __ldcg).  The counter wraps back
+// to 0 with the last.  flag: a word of shared memory.
+__device__ __forceinline__ bool arrive_last(unsigned* counter, int states, int* flag) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) *flag = atomicInc(counter, (unsigned)states - 1u) == (unsigned)states - 1u;
+    __syncthreads();
+    __threadfence();
+    return *flag != 0;
+}
+
+// The segment that is cut for the first time between the shares of CTAs `block` and `block` + 1, for a join
+// in a kernel of its own.
 template <int UNIT>
 struct PagedCut {
-    int b, seg, c0, c1, first_slot;    // its CTAs c0 .. c1; slot of c0's partial state (2c for the others)
+    int b, seg, c0, c1, first_slot;
 
     __device__ __forceinline__ bool find(const PagedParams& p, int block) {
-        const int total = plan_total<UNIT>(p), share = plan_share(p, total);
+        int head;
+        const int total = plan_total<UNIT>(p, head), share = plan_share(p, total);
         const long long cut = (long long)(block + 1) * share;
         if (cut >= total) return false;
         int base;
-        plan_locate<UNIT>(p, (int)cut, b, base);
+        plan_locate<UNIT>(p, (int)cut, head, b, base);
         const int units = seq_units<UNIT>(p, b);
         seg = ((int)cut - base) / units;
         const int s0 = base + seg * units;
@@ -199,7 +225,38 @@ struct PagedCut {
         first_slot = 2 * c0 + (s0 == c0 * share ? 0 : 1);
         return true;
     }
-    __device__ __forceinline__ int slot(int c) const { return c == c0 ? first_slot : 2 * c; }
+};
+
+// The pages of a warp's tiles, H a turn: every lane holds one entry, looked up a batch of 32 / H turns
+// ahead, so that no request waits for the table.
+template <int H>
+struct PageAhead {
+    static constexpr int kTurns = 32 / H;
+    const int* table;
+    int key, step, len, shift, now, then;      // key: of this lane's tile in turn 0
+
+    __device__ __forceinline__ void start(const PagedParams& p, const int* row, int key00, int unit, int n_keys, int turns) {
+        const int lane = threadIdx.x & 31;
+        table = row;
+        key = key00 + (lane / H) * unit + (lane % H) * kTileKeys;
+        step = kTurns * unit;
+        len = n_keys;
+        shift = p.page_shift;
+        now = look_up(0);
+        then = turns > kTurns ? look_up(1) : 0;
+    }
+    __device__ __forceinline__ int look_up(int batch) const {
+        const int at = key + batch * step;
+        return at >= 0 && at < len ? __ldg(table + (at >> shift)) : 0;
+    }
+    // before the first page of turn i
+    __device__ __forceinline__ void turn(int i) {
+        if (i % kTurns == 0 && i > 0) {
+            now = then;
+            then = look_up(i / kTurns + 1);
+        }
+    }
+    __device__ __forceinline__ int page(int i, int x) const { return __shfl_sync(0xffffffffu, now, (i % kTurns) * H + x); }
 };
 
 // ------------------------------------------------------------------ warp-level pieces

@@ -128,6 +128,83 @@ __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, in
     if (c == 0) p.lse1[row] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// Joins the partial states of CTAs c0 .. c1 (first_slot, then 2c) into rows [row, row + rows), of which
+// this is one of `shares` CTAs.  `each` of the WARPS warps take a row, every each-th state in order, kBatch
+// loaded together, and meet in shared memory (WARPS * 33 float4).
+constexpr int kBatch = 8;
+
+template <int D, int PART, int WARPS>
+__device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, int first_slot, size_t row, int rows, int mine,
+                                          int shares, float4* scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int states = c1 - c0 + 1;
+    int each = 1;
+    while (each < WARPS && (each * kBatch * 4 < states || (each * kBatch < states && each * rows < WARPS * shares))) each *= 2;
+    const int part = warp & (each - 1), group = warp / each, groups = WARPS / each;
+    for (int r0 = mine * groups; r0 < rows; r0 += shares * groups) {
+        const int r = r0 + group;
+        float M = kNoMax, MV = kNoMax, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float Mn, float Vn, float4 q, float4 x) {     // a state, references moved to Mn and Vn before
+            const float f1 = ex2(q.y - Vn);
+            L = fmaf(q.z, ex2(q.x - Mn), L);
+            acc.x = fmaf(x.x, f1, acc.x);
+            acc.y = fmaf(x.y, f1, acc.y);
+            acc.z = fmaf(x.z, f1, acc.z);
+            acc.w = fmaf(x.w, f1, acc.w);
+        };
+        auto move = [&](float Mn, float Vn) {
+            const float f0 = ex2(MV - Vn);
+            L *= ex2(M - Mn);
+            acc.x *= f0;
+            acc.y *= f0;
+            acc.z *= f0;
+            acc.w *= f0;
+            M = Mn;
+            MV = Vn;
+        };
+        if (r < rows) {
+            for (int c = c0 + part; c <= c1; c += kBatch * each) {
+                float4 q[kBatch], x[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int ck = c + k * each;
+                    q[k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (ck <= c1) {
+                        const float* from = p.part + (size_t)(ck == c0 ? first_slot : 2 * ck) * PART + r * (D + 4);
+                        q[k] = __ldcg(reinterpret_cast<const float4*>(from + D));
+                        x[k] = __ldcg(reinterpret_cast<const float4*>(from + 4 * (lane % (D / 4))));
+                    }
+                }
+                float Mn = M, Vn = MV;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    Mn = fmaxf(Mn, q[k].x);
+                    Vn = fmaxf(Vn, q[k].y);
+                }
+                move(Mn, Vn);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) add(Mn, Vn, q[k], x[k]);
+            }
+        }
+        if (each > 1) {
+            __syncthreads();
+            scratch[warp * 33 + lane] = acc;
+            if (lane == 0) scratch[warp * 33 + 32] = make_float4(M, MV, L, 0.f);
+            __syncthreads();
+            if (part == 0)
+                for (int w = warp + 1; w < warp + each; ++w) {
+                    const float4 q = scratch[w * 33 + 32], x = scratch[w * 33 + lane];
+                    const float Mn = fmaxf(M, q.x), Vn = fmaxf(MV, q.y);
+                    move(Mn, Vn);
+                    add(Mn, Vn, q, x);
+                }
+        }
+        if (part == 0 && r < rows && lane < D / 4) attn_finish<D>(p, row + r, lane, acc, M, MV, L);
+    }
+}
+
 template <int D, bool F8, int NT>
 __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) streamkl_paged_attn_kernel(const PagedParams p) {
     using C = AttnCfg<D, F8, NT>;
@@ -146,16 +223,6 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     const uint32_t value_at = V::load_offset(lane);
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
 
-    // sequences without keys: zeros and -inf
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (threadIdx.x == 0 && (p.lengths[b] < 0 || p.lengths[b] > p.width * p.page_size)) g_page_status = 5;
-        if (seq_len(p, b) > 0) continue;
-        const size_t r0 = (size_t)b * p.Hkv * p.rows, n = (size_t)p.Hkv * p.rows;
-        for (size_t i = threadIdx.x; i < n * (D / 8); i += kPagedThreads)
-            reinterpret_cast<uint4*>(p.out + r0 * D)[i] = make_uint4(0, 0, 0, 0);
-        for (size_t i = threadIdx.x; i < n; i += kPagedThreads) p.lse1[r0 + i] = -INFINITY;
-    }
-
     PagedWalk<C::kUnit> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
@@ -165,26 +232,21 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         const int* table = p.table + (size_t)walk.b * p.width;
         const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
 
-        // The turn whose rows are requested next: its pages (looked up one turn before), pool rows and
-        // number of existing keys of each tile.
-        int page[H], row[H], valid[H];
+        // The turn whose rows are requested next: pool rows and number of existing keys of each tile.
+        int row[H], valid[H];
         uint32_t bad = 0;                                 // bit (turn % 16) * 2 + tile: no such page
-        auto look_up = [&](int i) {
-#pragma unroll
-            for (int x = 0; x < H; ++x) {
-                const int key = key00 + i * C::kUnit + x * kTileKeys;
-                page[x] = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
-            }
-        };
+        PageAhead<H> pages;
+        pages.start(p, table, key00, C::kUnit, len, n);
         auto request_keys = [&](int i, uint32_t dst) {
             if (i < n) {
                 bad &= ~(3u << ((i & 15) * 2));
+                pages.turn(i);
 #pragma unroll
                 for (int x = 0; x < H; ++x) {
-                    const int key = key00 + i * C::kUnit + x * kTileKeys;
-                    const bool there = (unsigned)page[x] < (unsigned)p.pages;
+                    const int key = key00 + i * C::kUnit + x * kTileKeys, page = pages.page(i, x);
+                    const bool there = (unsigned)page < (unsigned)p.pages;
                     valid[x] = there ? len - key : 0;
-                    row[x] = there && key < len ? (page[x] * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
+                    row[x] = there && key < len ? (page * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
                     if (!there) {
                         bad |= 1u << ((i & 15) * 2 + x);
                         if (lane == 0) g_page_status = 5;
@@ -192,7 +254,6 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     K::copy(dst + x * K::kBytes + key_to, keys + (size_t)row[x] * K::kRow, valid[x], lane);
                     if (F8 && lane == x) cp_async16(dst + C::kExps + x * kTileKeys, p.a.exps + row[x]);
                 }
-                look_up(i + 1);
             }
             cp_commit();
         };
@@ -206,7 +267,6 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
             }
             cp_commit();
         };
-        look_up(0);
 #pragma unroll
         for (int i = 0; i < C::kAhead; ++i) {
             request_keys(i, ring + 2 * i * C::kSlot);
@@ -647,101 +707,41 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                 if (c == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, MV, L, 0.f);
             }
         }
+        if (!whole && p.arrived) {
+            const int c0 = walk.c0(), c1 = walk.c1();
+            if (arrive_last(p.arrived + c0, c1 - c0 + 1, reinterpret_cast<int*>(stats)))
+                attn_join<D, C::kPart, kPagedWarps>(p, c0, c1, walk.first_slot(), qrow + row0, rows, 0, 1, reinterpret_cast<float4*>(smem));
+        }
         __syncthreads();
+    }
+    // sequences without keys: zeros and -inf
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (threadIdx.x == 0 && (p.lengths[b] < 0 || p.lengths[b] > p.width * p.page_size)) g_page_status = 5;
+        if (seq_len(p, b) > 0) continue;
+        const size_t r0 = (size_t)b * p.Hkv * p.rows, n = (size_t)p.Hkv * p.rows;
+        for (size_t i = threadIdx.x; i < n * (D / 8); i += kPagedThreads)
+            reinterpret_cast<uint4*>(p.out + r0 * D)[i] = make_uint4(0, 0, 0, 0);
+        for (size_t i = threadIdx.x; i < n; i += kPagedThreads) p.lse1[r0 + i] = -INFINITY;
     }
 }
 
-// Joins the partial states of the segments that were cut.  Block x looks at the boundary
-// between the shares of CTAs x and x + 1 and takes the segment that is cut there for the first
-// time; blockIdx.y and gridDim.y deal out its rows.  `each` warps take a row, every each-th state
-// each (in a fixed order), and meet in shared memory.
+// The join in a kernel of its own, for segments with so many states and rows that one CTA would be long at it.
+// Block x looks at the boundary between the shares of CTAs x and x + 1 and takes the segment that is cut
+// there for the first time; blockIdx.y and gridDim.y deal out its rows.
 constexpr int kJoinThreads = 256;
-constexpr int kBatch = 8;              // states a warp loads together
 
 template <int D, int NT, int UNIT>
 __global__ void __launch_bounds__(kJoinThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
-    constexpr int kRows = 8 * NT, kStride = D + 4, kPart = kRows * kStride, kWarps = kJoinThreads / 32;
-    __shared__ float st[kWarps][4];
-    __shared__ float4 ac[kWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kRows = 8 * NT, kPart = kRows * (D + 4);
+    __shared__ float4 scratch[kJoinThreads / 32 * 33];
     PagedCut<UNIT> cut;
     const bool mine = cut.find(p, blockIdx.x);            // needs the lengths only
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!mine) return;
     const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
     const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
-    const int rows = min(kRows, p.rows - row0), states = cut.c1 - cut.c0 + 1;
-    const int each = states <= 8 ? 1 : states <= 32 ? 4 : 8;
-    const int part = warp & (each - 1), group = warp / each, groups = kWarps / each;
-    for (int r0 = blockIdx.y * groups; r0 < rows; r0 += gridDim.y * groups) {
-        const int r = r0 + group;
-        float M = kNoMax, MV = kNoMax, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            for (int c = cut.c0 + part; c <= cut.c1; c += kBatch * each) {
-                float4 q[kBatch], x[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int ck = c + k * each;
-                    const float* from = p.part + (size_t)cut.slot(ck <= cut.c1 ? ck : c) * kPart + r * kStride;
-                    q[k] = *reinterpret_cast<const float4*>(from + D);
-                    x[k] = *reinterpret_cast<const float4*>(from + 4 * (lane % (D / 4)));
-                    if (ck > cut.c1) {
-                        q[k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
-                        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                }
-                float Mn = M, Vn = MV;
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    Mn = fmaxf(Mn, q[k].x);
-                    Vn = fmaxf(Vn, q[k].y);
-                }
-                const float f0 = ex2(MV - Vn);
-                L *= ex2(M - Mn);
-                acc.x *= f0;
-                acc.y *= f0;
-                acc.z *= f0;
-                acc.w *= f0;
-                M = Mn;
-                MV = Vn;
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const float f1 = ex2(q[k].y - Vn);
-                    L = fmaf(q[k].z, ex2(q[k].x - Mn), L);
-                    acc.x = fmaf(x[k].x, f1, acc.x);
-                    acc.y = fmaf(x[k].y, f1, acc.y);
-                    acc.z = fmaf(x[k].z, f1, acc.z);
-                    acc.w = fmaf(x[k].w, f1, acc.w);
-                }
-            }
-        }
-        if (each > 1) {
-            __syncthreads();
-            if (lane == 0) {
-                st[warp][0] = M;
-                st[warp][1] = MV;
-                st[warp][2] = L;
-            }
-            ac[warp][lane] = acc;
-            __syncthreads();
-            if (part == 0) {
-                for (int w = warp + 1; w < warp + each; ++w) {
-                    const float Mn = fmaxf(M, st[w][0]), Vn = fmaxf(MV, st[w][1]);
-                    const float4 x = ac[w][lane];
-                    L = L * ex2(M - Mn) + st[w][2] * ex2(st[w][0] - Mn);
-                    const float f0 = ex2(MV - Vn), f1 = ex2(st[w][1] - Vn);
-                    acc.x = acc.x * f0 + x.x * f1;
-                    acc.y = acc.y * f0 + x.y * f1;
-                    acc.z = acc.z * f0 + x.z * f1;
-                    acc.w = acc.w * f0 + x.w * f1;
-                    M = Mn;
-                    MV = Vn;
-                }
-            }
-        }
-        if (part == 0 && r < rows && lane < D / 4) attn_finish<D>(p, qrow + row0 + r, lane, acc, M, MV, L);
-    }
+    attn_join<D, kPart, kJoinThreads / 32>(p, cut.c0, cut.c1, cut.first_slot, qrow + row0, min(kRows, p.rows - row0), blockIdx.y,
+                                           gridDim.y, scratch);
 }
 
 }  // namespace skl

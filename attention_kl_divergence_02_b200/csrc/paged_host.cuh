@@ -5,6 +5,7 @@
 namespace {
 
 constexpr int kWholeUnits = 8;
+constexpr int kJoinApart = 256;      // states * rows of a segment beyond which the join is a kernel of its own
 constexpr int kPagedMaxCtas = 4;     // most resident CTAs per SM of any variant
 
 int page_shift_of(int n) {
@@ -15,6 +16,11 @@ int page_shift_of(int n) {
 
 // Blocks of 8, 16, 24 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
 int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+
+// The counters at the head of a workspace, one per CTA: a fixed size, so that every call keeps them in one
+// place; a GPU has at most kPagedMaxSms SMs here.
+constexpr int kPagedMaxSms = (int)(STREAMKL_PAGED_COUNTER_BYTES / sizeof(unsigned)) / kPagedMaxCtas;
+int paged_sms() { return std::min(num_sms(), kPagedMaxSms); }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -47,7 +53,7 @@ template <int UNIT>
 void paged_grid(skl::PagedParams* p, int ctas) {
     const long long units = ((long long)p->width * p->page_size + UNIT - 1) / UNIT;
     const long long segments = (long long)p->B * p->Hkv * p->rblocks;
-    p->grid = ctas * num_sms();
+    p->grid = ctas * paged_sms();
     p->whole = units <= kWholeUnits ? 1 : 0;
     if (p->whole) p->grid = (int)std::min<long long>(p->grid, segments);
 }
@@ -137,15 +143,18 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     p->page_shift = page_shift_of(c->page_size);
     p->causal = causal ? 1 : 0;
     p->sl2 = scale * 1.4426950408889634f;
-    p->part = static_cast<float*>(workspace);
+    p->arrived = static_cast<unsigned*>(workspace);
+    p->part = reinterpret_cast<float*>(static_cast<char*>(workspace) + STREAMKL_PAGED_COUNTER_BYTES);
     return STREAMKL_OK;
 }
 
+// A programmatic dependent of the main kernel: its CTAs come as that kernel's end, plan meanwhile, and wait
+// for the partial states.
 template <typename K>
-int launch_join(K kernel, int threads, const skl::PagedParams& p, int gy, cudaStream_t st, const char* what) {
+int launch_join(K kernel, const skl::PagedParams& p, int gy, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = dim3(skl::kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -153,7 +162,7 @@ int launch_join(K kernel, int threads, const skl::PagedParams& p, int gy, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-    if (e != cudaSuccess) return cuda_fail(e, what);
+    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_attn join launch");
     return STREAMKL_OK;
 }
 
@@ -163,12 +172,16 @@ int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     static_assert(C::kCtas <= kPagedMaxCtas, "workspace");
     static std::atomic<unsigned long long> done{0};
     paged_grid<C::kUnit>(&p, C::kCtas);
-    const int rc = launch_main(skl::streamkl_paged_attn_kernel<D, F8, NT>, C::kSmem, p, st, done, "streamkl_paged_attn launch");
-    if (rc || p.whole) return rc;
-    // few segments: each has many partial states, and its rows go to CTAs of their own
     const long long segments = (long long)p.B * p.Hkv * p.rblocks;
-    const int gy = segments * 16 <= p.grid ? std::min(p.rows, 8 * NT) : NT;
-    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, skl::kJoinThreads, p, gy, st, "streamkl_paged_attn join launch");
+    const long long states = (p.grid + segments - 1) / segments + 1;      // of a segment, about
+    const int rows = std::min(p.rows, 8 * NT);
+    const bool apart = !p.whole && states * rows > kJoinApart;
+    if (apart) p.arrived = nullptr;
+    const int rc = launch_main(skl::streamkl_paged_attn_kernel<D, F8, NT>, C::kSmem, p, st, done, "streamkl_paged_attn launch");
+    if (rc || !apart) return rc;
+    // where a segment has many states, each of its rows gets a CTA
+    const int gy = states > 16 ? rows : NT;
+    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, p, gy, st);
 }
 
 template <int D, bool F8>
@@ -187,9 +200,7 @@ int launch_paged_kl(skl::PagedParams p, cudaStream_t st) {
     static_assert(C::kCtas <= kPagedMaxCtas, "workspace");
     static std::atomic<unsigned long long> done{0};
     paged_grid<C::kUnit>(&p, C::kCtas);
-    const int rc = launch_main(skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>, C::kSmem, p, st, done, "streamkl_paged_kl launch");
-    if (rc || p.whole) return rc;
-    return launch_join(skl::streamkl_paged_kl_join_kernel<NT, C::kUnit>, skl::kPagedThreads, p, 1, st, "streamkl_paged_kl join launch");
+    return launch_main(skl::streamkl_paged_kl_kernel<D, F1, F2, SHARED, NT>, C::kSmem, p, st, done, "streamkl_paged_kl launch");
 }
 
 template <int D, bool F1, bool F2, bool SHARED>
@@ -226,7 +237,7 @@ int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int wid
 size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d) {
     if (B < 1 || Hq < 1 || Hkv < 1 || NQ < 1 || Hq % Hkv || (d != 64 && d != 128)) return 0;
     const long long rows = (long long)(Hq / Hkv) * NQ;
-    return (size_t)kPagedMaxCtas * num_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
+    return STREAMKL_PAGED_COUNTER_BYTES + (size_t)kPagedMaxCtas * paged_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
 }
 
 int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,

@@ -13,8 +13,8 @@
 // the work this shares.  There is no weighted sum of values, so every lane keeps scalars of its own
 // over the keys that it sees and no maximum crosses lanes until the segment ends.
 //
-// The last line is evaluated in fp64 (a few hundred rows): acc / l1 and the difference of the log
-// sums are each as large as the scores' spread and may cancel to a small divergence.
+// The last line is summed in fp64: its terms are as large as the scores' spread and may cancel to a small
+// divergence.
 #pragma once
 
 #include "paged.cuh"
@@ -69,11 +69,10 @@ __device__ __forceinline__ void kl_finish(const PagedParams& p, size_t row, cons
         p.lse1[row] = p.lse2[row] = -INFINITY;
         return;
     }
-    const double ln2 = 0.693147180559945309417;
-    const double g1 = log2((double)a[1]), g2 = log2((double)a[3]);
-    p.lse1[row] = (float)(ln2 * ((double)a[0] + g1));
-    p.lse2[row] = (float)(ln2 * ((double)a[2] + g2));
-    p.kl[row] = (float)(ln2 * ((double)a[4] / (double)a[1] + ((double)a[2] - (double)a[0]) + (g2 - g1)));
+    const float ln2 = 0.69314718056f;
+    p.lse1[row] = ln2 * (a[0] + log2f(a[1]));
+    p.lse2[row] = ln2 * (a[2] + log2f(a[3]));
+    p.kl[row] = (float)((double)ln2 * ((double)(a[4] / a[1]) + ((double)a[2] - (double)a[0]) + (double)log2f(a[3] / a[1])));
 }
 
 // S^T of one tile: c[nt] += K Q^T for every block of 8 query rows.  at: the lane's load offsets.
@@ -114,7 +113,6 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
     using K1 = typename C::K1;
     using K2 = typename C::K2;
     extern __shared__ __align__(128) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join's CTAs may come as SMs fall free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
     const uint32_t ring = sb + warp * C::kWarp;
@@ -126,16 +124,6 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
     const uint32_t at1[2] = {(uint32_t)K1::load_offset(lane, 0), (uint32_t)K1::load_offset(lane, K1::kChunks > 1)};
     const uint32_t at2[2] = {(uint32_t)K2::load_offset(lane, 0), (uint32_t)K2::load_offset(lane, K2::kChunks > 1)};
 
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (threadIdx.x == 0 && (p.lengths[b] < 0 || p.lengths[b] > p.width * p.page_size)) g_page_status = 5;
-        if (seq_len(p, b) > 0) continue;
-        const size_t r0 = (size_t)b * p.Hkv * p.rows, n = (size_t)p.Hkv * p.rows;
-        for (size_t i = threadIdx.x; i < n; i += kPagedThreads) {
-            p.kl[r0 + i] = 0.f;
-            p.lse1[r0 + i] = p.lse2[r0 + i] = -INFINITY;
-        }
-    }
-
     PagedWalk<C::kUnit> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
@@ -144,24 +132,19 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)walk.b * p.width;
         const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
-        int page[H];              // of the tiles that are requested next
         uint32_t bad = 0;         // bit (turn % 16) * 2 + tile: no such page
-        auto look_up = [&](int i) {
-#pragma unroll
-            for (int x = 0; x < H; ++x) {
-                const int key = key00 + i * C::kUnit + x * kTileKeys;
-                page[x] = key < len ? __ldg(table + (key >> p.page_shift)) : 0;
-            }
-        };
+        PageAhead<H> pages;
+        pages.start(p, table, key00, C::kUnit, len, n);
         auto request = [&](int i, uint32_t dst) {
             if (i < n) {
                 bad &= ~(3u << ((i & 15) * 2));
+                pages.turn(i);
 #pragma unroll
                 for (int x = 0; x < H; ++x) {
-                    const int key = key00 + i * C::kUnit + x * kTileKeys;
-                    const bool there = (unsigned)page[x] < (unsigned)p.pages;
+                    const int key = key00 + i * C::kUnit + x * kTileKeys, page = pages.page(i, x);
+                    const bool there = (unsigned)page < (unsigned)p.pages;
                     const int valid = there ? len - key : 0;
-                    const int row = there && key < len ? (page[x] * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
+                    const int row = there && key < len ? (page * p.Hkv + h) * p.page_size + (key & (p.page_size - 1)) : 0;
                     if (!there) {
                         bad |= 1u << ((i & 15) * 2 + x);
                         if (lane == 0) g_page_status = 5;
@@ -171,11 +154,9 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                     if (F1 && lane == x) cp_async16(dst + C::kExp1 + x * kTileKeys, p.a.exps + row);
                     if (F2 && !SHARED && lane == H + x) cp_async16(dst + C::kExp2 + x * kTileKeys, p.b.exps + row);
                 }
-                look_up(i + 1);
             }
             cp_commit();
         };
-        look_up(0);
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) request(i, ring + i * C::kStage);
 
@@ -356,8 +337,8 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                     for (int k = 0; k < 5; ++k) stats[(warp * 5 + k) * C::kRows + nt * 8 + 2 * t + j] = a[nt][j][k];
             }
         __syncthreads();
-        const int r = threadIdx.x;
-        if (r < min(C::kRows, p.rows - row0)) {
+        const int r = threadIdx.x, rows = min(C::kRows, p.rows - row0);
+        if (r < rows) {
             float x[5], y[5];
 #pragma unroll
             for (int k = 0; k < 5; ++k) x[k] = stats[k * C::kRows + r];
@@ -375,37 +356,43 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                 for (int k = 0; k < 5; ++k) to[k * C::kRows] = x[k];
             }
         }
+        if (!walk.complete()) {
+            const int c0 = walk.c0(), c1 = walk.c1();
+            if (arrive_last(p.arrived + c0, c1 - c0 + 1, reinterpret_cast<int*>(smem))) {
+                // a power of two of lanes to a row, every such state each
+                constexpr int kLanes = NT == 1 ? 16 : NT == 2 ? 8 : 4;
+                const int jr = threadIdx.x / kLanes, sub = threadIdx.x % kLanes, first_slot = walk.first_slot();
+                float x[5] = {kNoMax, 0.f, kNoMax, 0.f, 0.f}, y[5];
+                if (jr < rows) {
+#pragma unroll 4
+                    for (int c = c0 + sub; c <= c1; c += kLanes) {
+                        const float* from = p.part + (size_t)(c == c0 ? first_slot : 2 * c) * C::kPart + jr;
+#pragma unroll
+                        for (int k = 0; k < 5; ++k) y[k] = __ldcg(from + k * C::kRows);
+                        kl_join(x, y);
+                    }
+                }
+#pragma unroll
+                for (int d = kLanes / 2; d > 0; d >>= 1) {
+#pragma unroll
+                    for (int k = 0; k < 5; ++k) y[k] = __shfl_xor_sync(0xffffffffu, x[k], d);
+                    kl_join(x, y);
+                }
+                if (sub == 0 && jr < rows) kl_finish(p, qrow + row0 + jr, x);
+            }
+        }
         __syncthreads();
     }
-}
 
-// Joins the partial states of the segments that were cut; see streamkl_paged_attn_join_kernel.
-// A warp takes a row and its lanes the states.
-template <int NT, int UNIT>
-__global__ void __launch_bounds__(kPagedThreads) streamkl_paged_kl_join_kernel(const PagedParams p) {
-    constexpr int kRows = 8 * NT, kPart = kRows * 5;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    PagedCut<UNIT> cut;
-    const bool mine = cut.find(p, blockIdx.x);            // needs the lengths only
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
-    const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
-    const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
-    for (int r = warp; r < min(kRows, p.rows - row0); r += kPagedWarps) {
-        float x[5] = {kNoMax, 0.f, kNoMax, 0.f, 0.f}, y[5];
-        for (int c = cut.c0 + lane; c <= cut.c1; c += 32) {
-            const float* from = p.part + (size_t)cut.slot(c) * kPart + r;
-#pragma unroll
-            for (int k = 0; k < 5; ++k) y[k] = from[k * kRows];
-            kl_join(x, y);
+    // sequences without keys
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (threadIdx.x == 0 && (p.lengths[b] < 0 || p.lengths[b] > p.width * p.page_size)) g_page_status = 5;
+        if (seq_len(p, b) > 0) continue;
+        const size_t r0 = (size_t)b * p.Hkv * p.rows, n = (size_t)p.Hkv * p.rows;
+        for (size_t i = threadIdx.x; i < n; i += kPagedThreads) {
+            p.kl[r0 + i] = 0.f;
+            p.lse1[r0 + i] = p.lse2[r0 + i] = -INFINITY;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-#pragma unroll
-            for (int k = 0; k < 5; ++k) y[k] = __shfl_xor_sync(0xffffffffu, x[k], d);
-            kl_join(x, y);
-        }
-        if (lane == 0) kl_finish(p, qrow + row0 + r, x);
     }
 }
 

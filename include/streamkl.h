@@ -267,10 +267,15 @@ int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int wid
                           uint16_t* v, void* stream);
 
 /*
- * Bytes of workspace for streamkl_paged_attn and streamkl_paged_kl: two partial states per CTA of a
- * grid of four per SM of the current device, whatever the lengths are.  Returns 0 for sizes
- * outside the supported range.
+ * Bytes of workspace for streamkl_paged_attn and streamkl_paged_kl: a counter and two partial states per
+ * CTA of a grid of four per SM of the current device, whatever the lengths are.  Returns 0 for
+ * sizes outside the supported range.
+ *
+ * The counters, the first STREAMKL_PAGED_COUNTER_BYTES of a workspace, must be zero before its first use
+ * (cudaMemset once); every call leaves them zero, so one workspace serves calls of any sizes, one
+ * after another.  The rest may hold anything.
  */
+#define STREAMKL_PAGED_COUNTER_BYTES ((size_t)4096)
 size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
 
 /*
@@ -283,9 +288,9 @@ size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
  * A row that sees no key gets zeros and lse = -inf.  What lies in the cache behind a sequence's
  * length, or behind the last key that a row sees, does not reach the row's result even when it is
  * not finite.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
- *   workspace : at least streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d) bytes; contents on entry
- *               do not matter.  Two calls that run at the same time need two workspaces.
- * Two kernels; the result does not depend on the order in which CTAs run.
+ *   workspace : at least streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d) bytes, its counters zero (see
+ *               there).  Two calls that can run at the same time need two workspaces.
+ * One or two kernels; the result does not depend on the order in which CTAs run.
  */
 int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,
                         const int* lengths, int B, int Hq, int NQ, float scale, int causal,

@@ -16,6 +16,17 @@ def status():
     return binding.streamkl_device_status()
 
 
+def workspace(B, Hq, Hkv, NQ, d):
+    """NaN behind the counters."""
+    ws = binding.paged_workspace(B, Hq, Hkv, NQ, d)
+    ws[binding.PAGED_COUNTER_BYTES // 4:] = float("nan")
+    return ws
+
+
+def counters_are_zero(ws):
+    return not bool(ws[:binding.PAGED_COUNTER_BYTES // 4].view(torch.int32).any())
+
+
 def rows(lengths):
     """New rows [B, Hkv, NT, d] as the calls take them."""
     return max(1, max(lengths))
@@ -137,9 +148,10 @@ def test_attention(case):
     c = ref.Case(lengths, Hkv, d, page, kind, seed=11)
     q = ref.queries(len(lengths), Hq, NQ, d, seed=12)
     scale = 0.9 / math.sqrt(d)
-    ws = binding.paged_workspace(len(lengths), Hq, Hkv, NQ, d).fill_(float("nan"))
+    ws = workspace(len(lengths), Hq, Hkv, NQ, d)
     out, lse = binding.paged_attn(q, c.cache, c.table, c.len, scale=scale, causal=causal, workspace=ws)
     assert status() == binding.OK
+    assert counters_are_zero(ws)
     want, want_lse, tol, tol_lse = ref.attention(c, q, scale, causal)
     ref.close(out, want, tol, "out")
     ref.close(lse, want_lse, tol_lse, "lse")
@@ -310,9 +322,10 @@ def test_divergence(case):
     q1 = ref.queries(len(lengths), Hq, NQ, d, seed=22)
     q2 = ref.queries(len(lengths), Hq, NQ, d, seed=23, near=q1)
     scale = 0.9 / math.sqrt(d)
-    ws = binding.paged_workspace(len(lengths), Hq, Hkv, NQ, d).fill_(float("nan"))
+    ws = workspace(len(lengths), Hq, Hkv, NQ, d)
     got = binding.paged_kl(q1, c1.cache, q2, c2.cache, c1.table, c1.len, scale=scale, causal=causal, workspace=ws)
     assert status() == binding.OK
+    assert counters_are_zero(ws)
     kl, lse1, lse2, tol, tol_lse = ref.divergence(c1, q1, c2, q2, scale, causal)
     ref.close(got[0], kl, tol, "kl")
     ref.close(got[1], lse1, tol_lse, "lse1")

@@ -140,9 +140,9 @@ def test_caches_that_do_not_match(kw, want):
 
 def test_workspace_bytes():
     n = 4 * binding.streamkl_num_sms() * 2
-    assert binding.streamkl_paged_workspace_bytes(1, 8, 8, 1, 128) == n * 8 * 132 * 4
-    assert binding.streamkl_paged_workspace_bytes(64, 32, 8, 3, 64) == n * 16 * 68 * 4
-    assert binding.streamkl_paged_workspace_bytes(1, 32, 1, 9, 64) == n * 32 * 68 * 4
+    assert binding.streamkl_paged_workspace_bytes(1, 8, 8, 1, 128) == 4096 + n * 8 * 132 * 4
+    assert binding.streamkl_paged_workspace_bytes(64, 32, 8, 3, 64) == 4096 + n * 16 * 68 * 4
+    assert binding.streamkl_paged_workspace_bytes(1, 32, 1, 9, 64) == 4096 + n * 32 * 68 * 4
     for bad in ((0, 8, 8, 1, 128), (1, 8, 3, 1, 128), (1, 8, 8, 0, 128), (1, 8, 8, 1, 96)):
         assert binding.streamkl_paged_workspace_bytes(*bad) == 0
 
