@@ -193,13 +193,16 @@ private:
 
 // Called by all threads of a CTA once its partial state of a segment is written: true in the one that
 // comes last of `states`, which then may read them all (past L1, __ldcg).  The counter wraps back
-// to 0 with the last.  flag: a word of shared memory.
+// to 0 with the last.  One thread's release carries the writes that the barrier put before it, and its
+// acquire, behind the second barrier, lets the others read.  flag: a word of shared memory.
 __device__ __forceinline__ bool arrive_last(unsigned* counter, int states, int* flag) {
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) *flag = atomicInc(counter, (unsigned)states - 1u) == (unsigned)states - 1u;
+    if (threadIdx.x == 0) {
+        unsigned before;
+        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(before) : "l"(counter), "r"((unsigned)states - 1u) : "memory");
+        *flag = before == (unsigned)states - 1u;
+    }
     __syncthreads();
-    __threadfence();
     return *flag != 0;
 }
 
@@ -406,53 +409,59 @@ __device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {   // 0 for inf
     return x >= 0x7f80u ? 0.f : __uint_as_float(x << 16);
 }
 
-// B fragments of 8 query rows (row0 .. row0 + 7 of the KV head's contiguous rows; rows past `rows`
-// are zeros) for KeyTile<D, F8>: frag[s] of every k-step, and the lane's factor by which a product
-// is turned into a score in base 2 (of row lane / 4).
+// 8 query rows as B fragments for KeyTile<D, F8>, in two steps: the loads are issued before a segment's first
+// keys are requested, or they would queue behind the megabytes that all CTAs request at once (measured:
+// 5 us instead of under 1), and turned into fragments after.
 template <int D, bool F8>
-__device__ __forceinline__ void load_queries(const uint16_t* q, int row0, int rows, float sl2, uint2* frag, float& factor) {
-    using K = KeyTile<D, F8>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const bool have = row0 + g < rows;
-    const uint16_t* src = q + (size_t)(row0 + g) * D;
-    constexpr int kLoads = D / 32;      // 16-byte loads of a row per lane
+struct Queries {
+    static constexpr int kLoads = D / 32;      // 16-byte loads of a row per lane
     uint4 v[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-        // bf16 keys: chunk u covers columns [32u + 8t, +8); e4m3: [64(u/2) + 16t + 8(u%2), +8)
-        const int col = F8 ? (u >> 1) * 64 + t * 16 + (u & 1) * 8 : u * 32 + t * 8;
-        v[u] = have ? __ldg(reinterpret_cast<const uint4*>(src + col)) : make_uint4(0, 0, 0, 0);
-    }
-    factor = sl2;
-    if (!F8) {
+
+    // rows row0 .. row0 + 7 of the KV head's contiguous rows q; rows past `rows` are zeros
+    __device__ __forceinline__ void load(const uint16_t* q, int row0, int rows) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const bool have = row0 + g < rows;
+        const uint16_t* src = q + (size_t)(row0 + g) * D;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            frag[2 * u] = make_uint2(v[u].x, v[u].y);
-            frag[2 * u + 1] = make_uint2(v[u].z, v[u].w);
+            // bf16 keys: chunk u covers columns [32u + 8t, +8); e4m3: [64(u/2) + 16t + 8(u%2), +8)
+            const int col = F8 ? (u >> 1) * 64 + t * 16 + (u & 1) * 8 : u * 32 + t * 8;
+            v[u] = have ? __ldg(reinterpret_cast<const uint4*>(src + col)) : make_uint4(0, 0, 0, 0);
         }
-        return;
     }
-    float top = 0.f;
+    // frag[s] of every k-step; returns the lane's factor by which a product is turned into a score in base 2 (of
+    // row lane / 4)
+    __device__ __forceinline__ float fragments(float sl2, uint2* frag) const {
+        if (!F8) {
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            for (int u = 0; u < kLoads; ++u) {
+                frag[2 * u] = make_uint2(v[u].x, v[u].y);
+                frag[2 * u + 1] = make_uint2(v[u].z, v[u].w);
+            }
+            return sl2;
+        }
+        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(finite_abs(w[i]), finite_abs(w[i] >> 16)));
+        for (int u = 0; u < kLoads; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(finite_abs(w[i]), finite_abs(w[i] >> 16)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = query_exponent(top);
+        const float inv = pow2(-e);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = pack_half(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+            frag[2 * u] = make_uint2(h[0], h[1]);
+            frag[2 * u + 1] = make_uint2(h[2], h[3]);
+        }
+        return fmaxf(pow2(e) * sl2, 1.17549435e-38f);
     }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = query_exponent(top);
-    const float inv = pow2(-e);
-    factor = fmaxf(pow2(e) * sl2, 1.17549435e-38f);
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = pack_half(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
-        frag[2 * u] = make_uint2(h[0], h[1]);
-        frag[2 * u + 1] = make_uint2(h[2], h[3]);
-    }
-}
+};
 
 }  // namespace skl

@@ -232,6 +232,14 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         const int* table = p.table + (size_t)walk.b * p.width;
         const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
 
+        Queries<D, F8> raw[C::kSharedQ ? 1 : NT];
+        if (C::kSharedQ) {
+            raw[0].load(p.q1 + qrow * D, row0 + 8 * warp, p.rows);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) raw[C::kSharedQ ? 0 : nt].load(p.q1 + qrow * D, row0 + 8 * nt, p.rows);
+        }
+
         // The turn whose rows are requested next: pool rows and number of existing keys of each tile.
         int row[H], valid[H];
         uint32_t bad = 0;                                 // bit (turn % 16) * 2 + tile: no such page
@@ -278,8 +286,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         float fac[NT][2];
         if (C::kSharedQ) {
             uint2 f[C::kSteps];
-            float one;
-            load_queries<D, F8>(p.q1 + qrow * D, row0 + 8 * warp, p.rows, p.sl2, f, one);
+            const float one = raw[0].fragments(p.sl2, f);
             if (warp < NT) {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s)
@@ -295,8 +302,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float one;
-                load_queries<D, F8>(p.q1 + qrow * D, row0 + 8 * nt, p.rows, p.sl2, qf + nt * C::kSteps, one);
+                const float one = raw[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf + (C::kSharedQ ? 0 : nt * C::kSteps));
                 fac[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
                 fac[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }

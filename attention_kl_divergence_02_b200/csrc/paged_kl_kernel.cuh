@@ -132,6 +132,14 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)walk.b * p.width;
         const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
+        Queries<D, F1> raw1[C::kSharedQ ? 1 : NT];
+        Queries<D, F2> raw2[C::kSharedQ ? 1 : NT];
+#pragma unroll
+        for (int nt = 0; nt < (C::kSharedQ ? 1 : NT); ++nt) {
+            const int at = row0 + 8 * (C::kSharedQ ? warp : nt);
+            raw1[nt].load(p.q1 + qrow * D, at, p.rows);
+            raw2[nt].load(p.q2 + qrow * D, at, p.rows);
+        }
         uint32_t bad = 0;         // bit (turn % 16) * 2 + tile: no such page
         PageAhead<H> pages;
         pages.start(p, table, key00, C::kUnit, len, n);
@@ -164,16 +172,15 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         float fac1[NT][2], fac2[NT][2];
         if (C::kSharedQ) {
             uint2 f[C::kSteps];
-            float one;
             float* fs = reinterpret_cast<float*>(smem + C::kFactor);
             uint2* qs = reinterpret_cast<uint2*>(smem + C::kQ);
-            load_queries<D, F1>(p.q1 + qrow * D, row0 + 8 * warp, p.rows, p.sl2, f, one);
+            float one = raw1[0].fragments(p.sl2, f);
             if (warp < NT) {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s) qs[(warp * C::kSteps + s) * 32 + lane] = f[s];
                 if (t == 0) fs[warp * 8 + g] = one;
             }
-            load_queries<D, F2>(p.q2 + qrow * D, row0 + 8 * warp, p.rows, p.sl2, f, one);
+            one = raw2[0].fragments(p.sl2, f);
             if (warp < NT) {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s) qs[((NT + warp) * C::kSteps + s) * 32 + lane] = f[s];
@@ -190,11 +197,10 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float one;
-                load_queries<D, F1>(p.q1 + qrow * D, row0 + 8 * nt, p.rows, p.sl2, qf1 + nt * C::kSteps, one);
+                float one = raw1[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf1 + (C::kSharedQ ? 0 : nt * C::kSteps));
                 fac1[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
                 fac1[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
-                load_queries<D, F2>(p.q2 + qrow * D, row0 + 8 * nt, p.rows, p.sl2, qf2 + nt * C::kSteps, one);
+                one = raw2[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf2 + (C::kSharedQ ? 0 : nt * C::kSteps));
                 fac2[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
                 fac2[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }
