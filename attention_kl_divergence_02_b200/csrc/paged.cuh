@@ -68,58 +68,62 @@ __device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-// UNIT: keys of a unit, all warps' tiles once.
-template <int UNIT>
-__device__ __forceinline__ int seq_units(const PagedParams& p, int b) {
-    return (seq_len(p, b) + UNIT - 1) / UNIT;
-}
-
-// T: units of all segments.  Each warp computes it by itself, as the rest of the plan: 32 sequences at a
-// time, without a barrier.  head: units of sequence `lane`, which most batches need not read again.
-template <int UNIT>
-__device__ __forceinline__ int plan_total(const PagedParams& p, int& head) {
-    const int lane = threadIdx.x & 31;
-    int n = head = lane < p.B ? seq_units<UNIT>(p, lane) : 0;
-    for (int b = lane + 32; b < p.B; b += 32) n += seq_units<UNIT>(p, b);
-    return __reduce_add_sync(0xffffffffu, n) * p.Hkv * p.rblocks;
-}
-
-// The share of a CTA.
-__device__ __forceinline__ int plan_share(const PagedParams& p, int total) {
-    return max((total + p.grid - 1) / p.grid, 1);
-}
-
-// The sequence that holds unit g (0 <= g < T), and the first unit of that sequence.
-template <int UNIT>
-__device__ __forceinline__ void plan_locate(const PagedParams& p, int g, int head, int& b, int& base) {
-    const int lane = threadIdx.x & 31, per = p.Hkv * p.rblocks;
-    int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int x = (b0 == 0 ? head : b0 + lane < p.B ? seq_units<UNIT>(p, b0 + lane) : 0) * per;
-        int upto = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const unsigned behind = __ballot_sync(0xffffffffu, g < before + upto);
-        if (behind) {
-            const int at = __ffs(behind) - 1;
-            b = b0 + at;
-            base = before + __shfl_sync(0xffffffffu, upto - x, at);
-            return;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+// UNIT: keys of a unit, all warps' tiles once.  START: units' worth of time that a CTA spends on beginning and
+// ending a segment; shares are equal in units plus START per segment, or a CTA with two segments would
+// end late by that much.  On the line of all segments, each is START + units long.
+template <int UNIT, int START>
+struct PagedPlan {
+    // of sequence b's segments
+    __device__ static __forceinline__ int units(int len) { return (len + UNIT - 1) / UNIT; }
+    __device__ static __forceinline__ int length(const PagedParams& p, int b) {
+        const int n = units(seq_len(p, b));
+        return n ? n + START : 0;
     }
-    b = base = 0;      // not reached for g < T
-}
 
-// A CTA's walk over its work: whole segments in turn where all are short (p.whole), else its share of
-// all units, cut where it begins and ends.
-template <int UNIT>
+    // Length of the whole line.  Each warp computes it by itself, as the rest of the plan: 32 sequences at a
+    // time, without a barrier.  head: of sequence `lane`, which most batches need not read again.
+    __device__ static __forceinline__ int total(const PagedParams& p, int& head) {
+        const int lane = threadIdx.x & 31;
+        int n = head = lane < p.B ? length(p, lane) : 0;
+        for (int b = lane + 32; b < p.B; b += 32) n += length(p, b);
+        return __reduce_add_sync(0xffffffffu, n) * p.Hkv * p.rblocks;
+    }
+
+    // The share of a CTA.
+    __device__ static __forceinline__ int share(const PagedParams& p, int total) { return max((total + p.grid - 1) / p.grid, 1); }
+
+    // The sequence at position g of the line, and where it begins.
+    __device__ static __forceinline__ void locate(const PagedParams& p, int g, int head, int& b, int& base) {
+        const int lane = threadIdx.x & 31, per = p.Hkv * p.rblocks;
+        int before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int x = (b0 == 0 ? head : b0 + lane < p.B ? length(p, b0 + lane) : 0) * per;
+            int upto = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const unsigned behind = __ballot_sync(0xffffffffu, g < before + upto);
+            if (behind) {
+                const int at = __ffs(behind) - 1;
+                b = b0 + at;
+                base = before + __shfl_sync(0xffffffffu, upto - x, at);
+                return;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        b = base = 0;      // not reached for g < total
+    }
+};
+
+// A CTA's walk over its work: whole segments in turn where all are short (p.whole), else its share of the
+// line, cut where it begins and ends.
+template <int UNIT, int START>
 struct PagedWalk {
+    using Plan = PagedPlan<UNIT, START>;
     int b, len, seg, units, u0, n;     // sequence, its keys, segment in it, its units, first unit and number of them to do
-    int pos, base, end, first, share;
+    int pos, base, end, first, share;  // position on the line, where the sequence begins, end and begin of the share
 
     __device__ __forceinline__ bool start(const PagedParams& p) {
         if (p.whole) {
@@ -128,52 +132,52 @@ struct PagedWalk {
             return find_whole(p);
         }
         int head;
-        const int total = plan_total<UNIT>(p, head);
-        share = plan_share(p, total);
+        const int total = Plan::total(p, head);
+        share = Plan::share(p, total);
         const long long at = (long long)blockIdx.x * share;
         if (at >= total) return false;
         first = pos = (int)at;
         end = (int)min((long long)total, at + share);
-        plan_locate<UNIT>(p, pos, head, b, base);
+        Plan::locate(p, pos, head, b, base);
         len = seq_len(p, b);
-        units = (len + UNIT - 1) / UNIT;
-        cut();
-        return true;
+        units = Plan::units(len);
+        return cut() || next(p);
     }
     __device__ __forceinline__ bool next(const PagedParams& p) {
         if (p.whole) {
             pos += gridDim.x;
             return find_whole(p);
         }
-        pos += n;
-        if (pos >= end) return false;
-        if (pos - base == units * p.Hkv * p.rblocks) {
-            base = pos;
-            do {
-                len = seq_len(p, ++b);
-            } while (len == 0);
-            units = (len + UNIT - 1) / UNIT;
-        }
-        cut();
+        do {
+            pos = base + (seg + 1) * (START + units);
+            if (pos >= end) return false;
+            if (seg + 1 == p.Hkv * p.rblocks) {
+                base = pos;
+                do {
+                    len = seq_len(p, ++b);
+                } while (len == 0);
+                units = Plan::units(len);
+            }
+        } while (!cut());
         return true;
     }
     __device__ __forceinline__ bool complete() const { return n == units; }
     // Where this CTA's partial state of the segment goes, and the segment's CTAs; their states are the first's
     // at first_slot() and the others' at 2c.
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (pos == first ? 0 : 1); }
-    __device__ __forceinline__ int c0() const { return (base + seg * units) / share; }
-    __device__ __forceinline__ int c1() const { return (base + seg * units + units - 1) / share; }
-    __device__ __forceinline__ int first_slot() const {
-        const int s0 = base + seg * units, c = s0 / share;
-        return 2 * c + (s0 == c * share ? 0 : 1);
-    }
+    __device__ __forceinline__ int c0() const { return (begin() + START) / share; }
+    __device__ __forceinline__ int c1() const { return (begin() + START + units - 1) / share; }
+    __device__ __forceinline__ int first_slot() const { return 2 * c0() + (begin() > c0() * share ? 1 : 0); }
 
 private:
-    __device__ __forceinline__ void cut() {
-        const int off = pos - base;
-        seg = off / units;
-        u0 = off - seg * units;
-        n = min(units - u0, end - pos);
+    __device__ __forceinline__ int begin() const { return base + seg * (START + units); }
+    // the units at pos; false where the share ends before the segment's first
+    __device__ __forceinline__ bool cut() {
+        seg = (pos - base) / (START + units);
+        const int unit0 = begin() + START;      // of unit 0 on the line
+        u0 = max(pos - unit0, 0);
+        n = min(end - unit0, units) - u0;
+        return n > 0;
     }
     __device__ __forceinline__ bool find_whole(const PagedParams& p) {
         const int per = p.Hkv * p.rblocks;
@@ -182,7 +186,7 @@ private:
             seg = pos - b * per;
             len = seq_len(p, b);
             if (len > 0) {
-                n = units = (len + UNIT - 1) / UNIT;
+                n = units = Plan::units(len);
                 u0 = 0;
                 return true;
             }
@@ -206,27 +210,27 @@ __device__ __forceinline__ bool arrive_last(unsigned* counter, int states, int* 
     return *flag != 0;
 }
 
-// The segment that is cut for the first time between the shares of CTAs `block` and `block` + 1, for a join
-// in a kernel of its own.
-template <int UNIT>
+// The segment whose units begin in CTA `block`'s share and end in a later one's, for a join in a kernel of
+// its own.
+template <int UNIT, int START>
 struct PagedCut {
+    using Plan = PagedPlan<UNIT, START>;
     int b, seg, c0, c1, first_slot;
 
     __device__ __forceinline__ bool find(const PagedParams& p, int block) {
         int head;
-        const int total = plan_total<UNIT>(p, head), share = plan_share(p, total);
+        const int total = Plan::total(p, head), share = Plan::share(p, total);
         const long long cut = (long long)(block + 1) * share;
         if (cut >= total) return false;
         int base;
-        plan_locate<UNIT>(p, (int)cut, head, b, base);
-        const int units = seq_units<UNIT>(p, b);
-        seg = ((int)cut - base) / units;
-        const int s0 = base + seg * units;
-        if (s0 == (int)cut || s0 / share != block) return false;    // not cut here, or cut before
-        c0 = block;
-        c1 = (s0 + units - 1) / share;
-        first_slot = 2 * c0 + (s0 == c0 * share ? 0 : 1);
-        return true;
+        Plan::locate(p, (int)cut, head, b, base);
+        const int units = Plan::units(seq_len(p, b));
+        seg = ((int)cut - base) / (START + units);
+        const int begin = base + seg * (START + units);
+        c0 = (begin + START) / share;
+        c1 = (begin + START + units - 1) / share;
+        first_slot = 2 * c0 + (begin > c0 * share ? 1 : 0);
+        return c0 == block && c1 > block;
     }
 };
 

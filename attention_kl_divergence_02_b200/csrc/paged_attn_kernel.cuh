@@ -90,6 +90,7 @@ struct AttnCfg {
     static constexpr int kCtas = NT == 1 ? 3 : 2;                      // on an SM
     static constexpr int kKeys = H * kTileKeys;                        // of a warp at a time
     static constexpr int kUnit = kPagedWarps * kKeys;
+    static constexpr int kStart = NT == 1 ? 4 : 6;                                   // see PagedPlan
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
     // A slot holds the keys or the values of kKeys tokens, and their exponents.  The slots form a ring,
@@ -211,7 +212,6 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     using K = typename C::K;
     using V = typename C::V;
     extern __shared__ __align__(128) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join's CTAs may come as SMs fall free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t sb = smem_u32(smem);
     const uint32_t ring = sb + warp * C::kWarp;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     const uint32_t value_at = V::load_offset(lane);
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
 
-    PagedWalk<C::kUnit> walk;
+    PagedWalk<C::kUnit, C::kStart> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
         const int h = walk.seg / p.rblocks, rb = walk.seg - h * p.rblocks;
@@ -736,14 +736,13 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 // there for the first time; blockIdx.y and gridDim.y deal out its rows.
 constexpr int kJoinThreads = 256;
 
-template <int D, int NT, int UNIT>
+template <int D, int NT, int UNIT, int START>
 __global__ void __launch_bounds__(kJoinThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
     constexpr int kRows = 8 * NT, kPart = kRows * (D + 4);
     __shared__ float4 scratch[kJoinThreads / 32 * 33];
-    PagedCut<UNIT> cut;
-    const bool mine = cut.find(p, blockIdx.x);            // needs the lengths only
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");    // the main kernel is complete, its states are visible
+    PagedCut<UNIT, START> cut;
+    if (!cut.find(p, blockIdx.x)) return;
     const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
     const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
     attn_join<D, kPart, kJoinThreads / 32>(p, cut.c0, cut.c1, cut.first_slot, qrow + row0, min(kRows, p.rows - row0), blockIdx.y,

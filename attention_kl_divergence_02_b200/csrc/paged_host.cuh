@@ -104,13 +104,12 @@ int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, co
     const int grid = (int)((warps + per - 1) / per);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool f8 = c->type == STREAMKL_CACHE_E4M3;
-#define SKL_CACHE(D, F8)                                                                          \
-    (append ? skl::streamkl_cache_append_kernel<D, F8><<<grid, skl::kCacheThreads, 0, st>>>(p)    \
-            : skl::streamkl_cache_gather_kernel<D, F8><<<grid, skl::kCacheThreads, 0, st>>>(p))
-    if (c->d == 128) f8 ? SKL_CACHE(128, true) : SKL_CACHE(128, false);
-    else f8 ? SKL_CACHE(64, true) : SKL_CACHE(64, false);
-#undef SKL_CACHE
-    cudaError_t e = cudaGetLastError();
+    auto kernel = c->d == 128 ? (f8 ? (append ? skl::streamkl_cache_append_kernel<128, true> : skl::streamkl_cache_gather_kernel<128, true>)
+                                    : (append ? skl::streamkl_cache_append_kernel<128, false> : skl::streamkl_cache_gather_kernel<128, false>))
+                              : (f8 ? (append ? skl::streamkl_cache_append_kernel<64, true> : skl::streamkl_cache_gather_kernel<64, true>)
+                                    : (append ? skl::streamkl_cache_append_kernel<64, false> : skl::streamkl_cache_gather_kernel<64, false>));
+    kernel<<<grid, skl::kCacheThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, append ? "streamkl_cache_append launch" : "streamkl_cache_gather launch");
     return STREAMKL_OK;
 }
@@ -127,7 +126,7 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     const long long rows = (long long)(Hq / c->Hkv) * NQ;
     const int nt = paged_row_tiles(rows);
     const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
-    const long long most = ((long long)width * c->page_size + 63) / 64;   // the smallest unit
+    const long long most = ((long long)width * c->page_size + 63) / 64 + 16;   // the smallest unit; PagedPlan's START
     if ((double)B * c->Hkv * (double)rblocks * (double)most >= 2147483648.0) return STREAMKL_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < streamkl_paged_workspace_bytes(B, Hq, c->Hkv, NQ, c->d))
         return STREAMKL_ERR_INVALID_ARG;
@@ -148,24 +147,6 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     return STREAMKL_OK;
 }
 
-// A programmatic dependent of the main kernel: its CTAs come as that kernel's end, plan meanwhile, and wait
-// for the partial states.
-template <typename K>
-int launch_join(K kernel, const skl::PagedParams& p, int gy, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
-    cfg.blockDim = dim3(skl::kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-    if (e != cudaSuccess) return cuda_fail(e, "streamkl_paged_attn join launch");
-    return STREAMKL_OK;
-}
-
 template <int D, bool F8, int NT>
 int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     using C = skl::AttnCfg<D, F8, NT>;
@@ -181,7 +162,18 @@ int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     if (rc || !apart) return rc;
     // where a segment has many states, each of its rows gets a CTA
     const int gy = states > 16 ? rows : NT;
-    return launch_join(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit>, p, gy, st);
+    // a programmatic dependent: its launch overlaps the main kernel's last CTAs, and it waits for them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
+    cfg.blockDim = dim3(skl::kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit, C::kStart>, p);
+    return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "streamkl_paged_attn join launch");
 }
 
 template <int D, bool F8>
@@ -208,7 +200,7 @@ int launch_paged_kl_rows(const skl::PagedParams& p, cudaStream_t st) {
     switch (paged_row_tiles(p.rows)) {
         case 1: return launch_paged_kl<D, F1, F2, SHARED, 1>(p, st);
         case 2: return launch_paged_kl<D, F1, F2, SHARED, 2>(p, st);
-        case 3: return launch_paged_kl<D, F1, F2, SHARED, 3>(p, st);
+        case 3:       // 17 to 24 rows: nothing to gain from a variant of their own, the keys' bytes bound them
         default: return launch_paged_kl<D, F1, F2, SHARED, 4>(p, st);
     }
 }

@@ -35,6 +35,7 @@ struct KlCfg {
     static constexpr int H = NT <= 2 && kTiles <= 3072 ? 2 : 1;
     static constexpr int kKeys = H * kTileKeys;
     static constexpr int kUnit = kPagedWarps * kKeys;
+    static constexpr int kStart = 4;                                   // see PagedPlan
     static constexpr int kOff2 = H * K1::kBytes;
     static constexpr int kExp1 = H * kTiles;
     static constexpr int kExp2 = SHARED ? kExp1 : kExp1 + (F1 ? kKeys : 0);
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
     const uint32_t at1[2] = {(uint32_t)K1::load_offset(lane, 0), (uint32_t)K1::load_offset(lane, K1::kChunks > 1)};
     const uint32_t at2[2] = {(uint32_t)K2::load_offset(lane, 0), (uint32_t)K2::load_offset(lane, K2::kChunks > 1)};
 
-    PagedWalk<C::kUnit> walk;
+    PagedWalk<C::kUnit, C::kStart> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
         const int h = walk.seg / p.rblocks, rb = walk.seg - h * p.rblocks;
