@@ -19,7 +19,7 @@
 namespace skl {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheTurns = 8;
+constexpr int kCacheTurns = 4;
 
 template <int D>
 struct CacheCfg {

@@ -86,7 +86,7 @@ template <int D, bool F8, int NT>
 struct AttnCfg {
     using K = KeyTile<D, F8>;
     using V = ValueTile<D, F8>;
-    static constexpr int H = NT > 2 || (D == 128 && (!F8 || NT == 2)) ? 1 : 2;
+    static constexpr int H = NT == 4 || (NT == 3 && !F8) || (D == 128 && !F8) ? 1 : 2;
     static constexpr int kCtas = NT == 1 ? 3 : 2;                      // on an SM
     static constexpr int kKeys = H * kTileKeys;                        // of a warp at a time
     static constexpr int kUnit = kPagedWarps * kKeys;
