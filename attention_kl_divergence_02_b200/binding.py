@@ -508,7 +508,7 @@ def _enter(cache, stream):
     it runs on, the caller's `stream` (an object or a handle) or the device's current one."""
     if stream is None:
         guard = None
-        if cache.index != _torch.cuda.current_device():
+        if cache.index != _torch._C._cuda_getDevice():
             guard = _torch.cuda.device(cache.device)
             guard.__enter__()
         return guard, _torch._C._cuda_getCurrentRawStream(cache.index)
@@ -528,18 +528,18 @@ def _leave(guard):
 
 def _need(name, t, dtype, shape, cache):
     """Refuses a tensor that the kernels would misread; `shape` is a tuple."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s on %s)"
                          % (name, dtype, shape, cache.device, t.dtype, tuple(t.shape), t.device))
 
 
 def _width(table, B, cache):
     """Pages of a row of the table [B, width]."""
-    if table.dim() != 2 or table.shape[1] < 1:
+    shape = table.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("table must be int32 [B, width]")
-    width = table.shape[1]
-    _need("table", table, _torch.int32, (B, width), cache)
-    return width
+    _need("table", table, _torch.int32, (B, shape[1]), cache)
+    return shape[1]
 
 
 def _rows_shape(cache, k, v):
@@ -616,9 +616,9 @@ def _scratch(workspace, shape, cache):
         B, Hq, NQ, d = shape
         nbytes = streamkl_paged_workspace_bytes(B, Hq, cache.shape[1], NQ, d)
         return _new_workspace(nbytes, cache.device), nbytes
-    if workspace.get_device() != cache.index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % (cache.device,))
-    return workspace, workspace.numel() * workspace.element_size()
+    if workspace.dtype is not _torch.float32 or workspace.get_device() != cache.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous fp32 tensor on %s (see paged_workspace)" % (cache.device,))
+    return workspace, workspace.numel() * 4
 
 
 def paged_attn(q, cache, table, lengths, scale=None, causal=True, out=None, workspace=None, stream=None):
@@ -633,13 +633,13 @@ def paged_attn(q, cache, table, lengths, scale=None, causal=True, out=None, work
     _need("lengths", lengths, _torch.int32, (B,), cache)
     guard, handle = _enter(cache, stream)
     try:
+        workspace, nbytes = _scratch(workspace, shape, cache)
         if out is None:
-            o, lse = out = _torch.empty_like(q), _torch.empty((B, Hq, NQ), dtype=_torch.float32, device=cache.device)
+            o, lse = out = _torch.empty_like(q), workspace.new_empty((B, Hq, NQ))
         else:
             o, lse = out
             _need("out", o, _torch.bfloat16, shape, cache)
             _need("lse", lse, _torch.float32, (B, Hq, NQ), cache)
-        workspace, nbytes = _scratch(workspace, shape, cache)
         rc = load().streamkl_paged_attn(cache.ref, q.data_ptr(), table.data_ptr(), width, lengths.data_ptr(), B, Hq, NQ,
                                         d ** -0.5 if scale is None else scale, 1 if causal else 0, o.data_ptr(),
                                         lse.data_ptr(), workspace.data_ptr(), nbytes, handle)
@@ -664,13 +664,13 @@ def paged_kl(q1, cache1, q2, cache2, table, lengths, scale=None, causal=True, ou
     _need("lengths", lengths, _torch.int32, (B,), cache1)
     guard, handle = _enter(cache1, stream)
     try:
+        workspace, nbytes = _scratch(workspace, shape, cache1)
         if out is None:
-            out = _torch.empty((3, B, Hq, NQ), dtype=_torch.float32, device=cache1.device).unbind(0)
+            out = workspace.new_empty((3, B, Hq, NQ)).unbind(0)
         else:
             for name, o in zip(("kl", "lse1", "lse2"), out):
                 _need(name, o, _torch.float32, (B, Hq, NQ), cache1)
         kl, lse1, lse2 = out
-        workspace, nbytes = _scratch(workspace, shape, cache1)
         rc = load().streamkl_paged_kl(cache1.ref, q1.data_ptr(), cache2.ref, q2.data_ptr(), table.data_ptr(), width,
                                       lengths.data_ptr(), B, Hq, NQ, d ** -0.5 if scale is None else scale,
                                       1 if causal else 0, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
