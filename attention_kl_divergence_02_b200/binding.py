@@ -428,9 +428,27 @@ def bwd(mode, q1, k1, q2, k2, kl, lse1, lse2, dkl, scale=None, causal=False, out
 
 
 # ------------------------------------------------------------------ paged key-value cache
-# torch, from the first PagedCache on: these calls are made once per token, and an import statement, a
-# tuple or a device object in each check adds up to the time of a kernel.
+# torch, and the extension that does the everyday case of a call (csrc/fastcall.c; None where it was not
+# built), from the first PagedCache on: these calls are made once per token, and an import statement, a tuple
+# or a device object in each check adds up to the time of a kernel.
 _torch = None
+_fast = None
+
+
+def _start():
+    global _torch, _fast
+    import torch
+    _torch = torch
+    try:
+        from . import _fastcall
+    except ImportError:
+        return
+    lib = load()
+    _fastcall.setup(torch.bfloat16, torch.int32, torch.float32, torch.empty_like, torch._C._cuda_getDevice,
+                    torch._C._cuda_getCurrentRawStream,
+                    *(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.streamkl_paged_attn, lib.streamkl_paged_kl,
+                                                                      lib.streamkl_cache_append, lib.streamkl_cache_gather)))
+    _fast = _fastcall
 
 
 class PagedCache:
@@ -440,9 +458,9 @@ class PagedCache:
     them; page tables, lengths and positions are the caller's int32 tensors."""
 
     def __init__(self, k, v=None, k_exp=None, v_exp=None):
-        global _torch
         import torch
-        _torch = torch
+        if _torch is None:
+            _start()
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not k.is_cuda:
             raise ValueError("k must be a bf16 or float8_e4m3fn CUDA tensor [pages, Hkv, page_size, d]")
         quantised = k.dtype == torch.float8_e4m3fn
@@ -467,6 +485,7 @@ class PagedCache:
         self.struct = CacheStruct(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp),
                                   CACHE_E4M3 if quantised else CACHE_BF16, pages, page_size, Hkv, d)
         self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, pages, Hkv, page_size, d, quantised=False, values=True, device="cuda"):
@@ -557,6 +576,12 @@ def _rows_shape(cache, k, v):
 def cache_append(cache, k, v, table, start, count=None, stream=None):
     """Writes k, v (bf16 [B, Hkv, NT, d]) into the cache: row i < count[b] (NT without `count`) of
     sequence b at position start[b] + i.  table int32 [B, width], start and count int32 [B]."""
+    if stream is None and _fast is not None and start is not None:
+        rc = _fast.move(cache.address, cache.index, True, k, v, table, start, count)
+        if rc is not NotImplemented:
+            if rc != OK:
+                raise StreamKLError(rc, "streamkl_cache_append")
+            return
     B, _, NT, _ = _rows_shape(cache, k, v)
     width = _width(table, B, cache)
     _need("start", start, _torch.int32, (B,), cache)
@@ -576,6 +601,12 @@ def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=No
     """Reads rows back into (k, v), bf16 [B, Hkv, rows, d]: row i < count[b] is the cached row at position
     start[b] + i (from 0 without `start`); rows behind the count are left as they were (zeros in
     tensors allocated here)."""
+    if stream is None and out is not None and rows is None and _fast is not None and count is not None:
+        rc = _fast.move(cache.address, cache.index, False, out[0], out[1], table, start, count)
+        if rc is not NotImplemented:
+            if rc != OK:
+                raise StreamKLError(rc, "streamkl_cache_gather")
+            return out
     if out is None and (rows is None or rows < 1 or table.dim() != 2):
         raise ValueError("out, or rows of at least 1 and a table [B, width], are required")
     guard, handle = _enter(cache, stream)
@@ -625,6 +656,13 @@ def paged_attn(q, cache, table, lengths, scale=None, causal=True, out=None, work
     """Attention of new tokens over the cache: (out bf16 [B, Hq, NQ, d], lse fp32 [B, Hq, NQ]).  lengths int32
     [B] count the new tokens; causal: they are the last NQ and see their own past only.  `workspace`
     (paged_workspace) is allocated here when not given."""
+    if out is None and stream is None and _fast is not None:
+        done = _fast.attn(q, cache.address, cache.index, table, lengths, cache.shape[3] ** -0.5 if scale is None else scale,
+                          causal, workspace)
+        if done is not NotImplemented:
+            if done[0] != OK:
+                raise StreamKLError(done[0], "streamkl_paged_attn")
+            return done[1:]
     shape = _query_shape("q", q, cache)
     if cache.v is None:
         raise ValueError("this cache has no values")
@@ -654,6 +692,13 @@ def paged_kl(q1, cache1, q2, cache2, table, lengths, scale=None, causal=True, ou
     """KL(P1 || P2) of two attentions of the new tokens over paged key caches: (kl, lse1, lse2), fp32
     [B, Hq, NQ].  P1 from q1 and cache1's keys, P2 from q2 and cache2's; pass the same cache twice
     for shared keys.  Other arguments as paged_attn."""
+    if out is None and stream is None and _fast is not None and cache1.index == cache2.index:
+        done = _fast.kl(q1, cache1.address, q2, cache2.address, cache1.index, table, lengths,
+                        cache1.shape[3] ** -0.5 if scale is None else scale, causal, workspace)
+        if done is not NotImplemented:
+            if done[0] != OK:
+                raise StreamKLError(done[0], "streamkl_paged_kl")
+            return done[1]
     shape = _query_shape("q1", q1, cache1)
     if cache1.shape != cache2.shape or cache1.index != cache2.index:
         raise ValueError("both caches must agree in shape and device (%s on %s, %s on %s)"

@@ -5,6 +5,7 @@
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -12,6 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libstreamkl.so")
 MAIN = os.path.join(CSRC, "streamkl.cu")
 INCLUDE = os.path.join(ROOT, "include")
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+FASTCALL_MAIN = os.path.join(CSRC, "fastcall.c")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -42,8 +45,24 @@ def stale():
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def build_fastcall(force=False):
+    """Compile the CPython extension that shortens the paged calls, where Python's headers are installed (the
+    binding does without it)."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    made_of = (FASTCALL_MAIN, os.path.join(INCLUDE, "streamkl.h"))
+    if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(s) <= os.path.getmtime(FASTCALL) for s in made_of):
+        return FASTCALL
+    tmp = FASTCALL + ".tmp.%d" % os.getpid()
+    subprocess.check_call(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", include, "-I", INCLUDE, "-o", tmp, FASTCALL_MAIN])
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(force=False, verbose=False):
-    """Compile the library if any source is newer than it.  Returns the .so path."""
+    """Compile the library if any source is newer than it, and the binding's extension.  Returns the library's path."""
+    build_fastcall(force)
     if not force and not stale():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()

@@ -358,33 +358,39 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
 #pragma unroll
-                for (int u = 0; u < K::kChunks; ++u)
+                for (int u = 0; u < K::kChunks; ++u) {
+                    uint4 y[H][2];
 #pragma unroll
-                    for (int x = 0; x < H; ++x) {
-                        const uint32_t at = cur + x * K::kBytes + key_at[u & 1];
-                        const uint4 y0 = lds128(at + K::load_step(0, u)), y1 = lds128(at + K::load_step(1, u));
-                        const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
+                    for (int x = 0; x < H; ++x)
 #pragma unroll
-                        for (int w = 0; w < K::kSteps; ++w) {
-                            uint32_t a0, a1, a2, a3;
+                        for (int k = 0; k < 2; ++k) y[x][k] = lds128(cur + x * K::kBytes + key_at[u & 1] + K::load_step(k, u));
+#pragma unroll
+                    for (int w = 0; w < K::kSteps; ++w) {
+                        uint32_t a[H][4];
+#pragma unroll
+                        for (int x = 0; x < H; ++x) {
+                            const uint32_t w0[4] = {y[x][0].x, y[x][0].y, y[x][0].z, y[x][0].w};
+                            const uint32_t w1[4] = {y[x][1].x, y[x][1].y, y[x][1].z, y[x][1].w};
                             if (F8) {
-                                e4m3x4_half2(w0[w], a0, a2);
-                                e4m3x4_half2(w1[w], a1, a3);
+                                e4m3x4_half2(w0[w], a[x][0], a[x][2]);
+                                e4m3x4_half2(w1[w], a[x][1], a[x][3]);
                             } else {
-                                a0 = w0[(2 * w) & 3];
-                                a1 = w1[(2 * w) & 3];
-                                a2 = w0[(2 * w + 1) & 3];
-                                a3 = w1[(2 * w + 1) & 3];
-                            }
-                            const int step = u * K::kSteps + w;
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 q = C::kSharedQ ? lds64(sb + C::kQ + ((nt * C::kSteps + step) * 32 + lane) * 8)
-                                                            : qf[C::kSharedQ ? 0 : nt * C::kSteps + step];
-                                mma16816<F8>(s[x][nt], a0, a1, a2, a3, q.x, q.y);
+                                a[x][0] = w0[(2 * w) & 3];
+                                a[x][1] = w1[(2 * w) & 3];
+                                a[x][2] = w0[(2 * w + 1) & 3];
+                                a[x][3] = w1[(2 * w + 1) & 3];
                             }
                         }
+                        const int step = u * K::kSteps + w;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 q = C::kSharedQ ? lds64(sb + C::kQ + ((nt * C::kSteps + step) * 32 + lane) * 8)
+                                                        : qf[C::kSharedQ ? 0 : nt * C::kSteps + step];
+#pragma unroll
+                            for (int x = 0; x < H; ++x) mma16816<F8>(s[x][nt], a[x][0], a[x][1], a[x][2], a[x][3], q.x, q.y);
+                        }
                     }
+                }
                 if (F8) {
 #pragma unroll
                     for (int x = 0; x < H; ++x) {

@@ -14,8 +14,13 @@ int page_shift_of(int n) {
     return s;
 }
 
-// Blocks of 8, 16, 24 or 32 query rows: the fewest that hold a KV head's rows, 32 beyond.
-int paged_row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+// Query rows are folded in blocks of 8 n.  Attention: n = 1 to 4, the fewest blocks that hold a KV head's rows.
+// Divergence: 1 or 2; more rows are several blocks, which read the keys again, from L2, since the CTAs
+// that do the blocks of one head run side by side (FIGURE2).
+int paged_row_tiles(long long rows, bool divergence) {
+    const int most = divergence ? 2 : 4;
+    return (int)std::min<long long>((rows + 7) / 8, most);
+}
 
 // The counters at the head of a workspace, one per CTA: a fixed size, so that every call keeps them in one
 // place; a GPU has at most kPagedMaxSms SMs here.
@@ -116,7 +121,8 @@ int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, co
 
 // Checks and fills what attention and divergence share.
 int paged_params(const streamkl_cache* c, const int* table, int width, const int* lengths, int B, int Hq, int NQ,
-                 float scale, int causal, void* workspace, size_t workspace_bytes, skl::PagedParams* p) {
+                 float scale, int causal, bool divergence, void* workspace, size_t workspace_bytes,
+                 skl::PagedParams* p) {
     int rc = check_table(c, table, width, B);
     if (rc) return rc;
     if (!lengths || Hq < 1 || NQ < 1) return STREAMKL_ERR_INVALID_ARG;
@@ -124,7 +130,7 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     if (Hq % c->Hkv != 0) return STREAMKL_ERR_UNSUPPORTED;
     if ((long long)B * Hq * NQ >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
     const long long rows = (long long)(Hq / c->Hkv) * NQ;
-    const int nt = paged_row_tiles(rows);
+    const int nt = paged_row_tiles(rows, divergence);
     const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
     const long long most = ((long long)width * c->page_size + 63) / 64 + 16;   // the smallest unit; PagedPlan's START
     if ((double)B * c->Hkv * (double)rblocks * (double)most >= 2147483648.0) return STREAMKL_ERR_UNSUPPORTED;
@@ -178,7 +184,7 @@ int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
 
 template <int D, bool F8>
 int launch_paged_attn_rows(const skl::PagedParams& p, cudaStream_t st) {
-    switch (paged_row_tiles(p.rows)) {
+    switch (paged_row_tiles(p.rows, false)) {
         case 1: return launch_paged_attn<D, F8, 1>(p, st);
         case 2: return launch_paged_attn<D, F8, 2>(p, st);
         case 3: return launch_paged_attn<D, F8, 3>(p, st);
@@ -197,12 +203,8 @@ int launch_paged_kl(skl::PagedParams p, cudaStream_t st) {
 
 template <int D, bool F1, bool F2, bool SHARED>
 int launch_paged_kl_rows(const skl::PagedParams& p, cudaStream_t st) {
-    switch (paged_row_tiles(p.rows)) {
-        case 1: return launch_paged_kl<D, F1, F2, SHARED, 1>(p, st);
-        case 2: return launch_paged_kl<D, F1, F2, SHARED, 2>(p, st);
-        case 3:       // 17 to 24 rows: nothing to gain from a variant of their own, the keys' bytes bound them
-        default: return launch_paged_kl<D, F1, F2, SHARED, 4>(p, st);
-    }
+    return paged_row_tiles(p.rows, true) == 1 ? launch_paged_kl<D, F1, F2, SHARED, 1>(p, st)
+                                              : launch_paged_kl<D, F1, F2, SHARED, 2>(p, st);
 }
 
 template <int D>
@@ -229,7 +231,7 @@ int streamkl_cache_gather(const streamkl_cache* cache, const int* table, int wid
 size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d) {
     if (B < 1 || Hq < 1 || Hkv < 1 || NQ < 1 || Hq % Hkv || (d != 64 && d != 128)) return 0;
     const long long rows = (long long)(Hq / Hkv) * NQ;
-    return STREAMKL_PAGED_COUNTER_BYTES + (size_t)kPagedMaxCtas * paged_sms() * 2 * 8 * paged_row_tiles(rows) * (d + 4) * sizeof(float);
+    return STREAMKL_PAGED_COUNTER_BYTES + (size_t)kPagedMaxCtas * paged_sms() * 2 * 8 * paged_row_tiles(rows, false) * (d + 4) * sizeof(float);
 }
 
 int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const int* table, int width,
@@ -240,7 +242,7 @@ int streamkl_paged_attn(const streamkl_cache* cache, const uint16_t* q, const in
     if (rc) return rc;
     if (!aligned16(q) || !aligned16(out) || !aligned4(lse)) return STREAMKL_ERR_UNSUPPORTED;
     skl::PagedParams p = {};
-    if ((rc = paged_params(cache, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
+    if ((rc = paged_params(cache, table, width, lengths, B, Hq, NQ, scale, causal, false, workspace, workspace_bytes, &p)))
         return rc;
     p.a = {static_cast<const uint8_t*>(cache->k), cache->k_exp};
     p.b = {static_cast<const uint8_t*>(cache->v), cache->v_exp};
@@ -269,7 +271,7 @@ int streamkl_paged_kl(const streamkl_cache* cache1, const uint16_t* q1, const st
     if (!aligned16(q1) || !aligned16(q2) || !aligned4(kl) || !aligned4(lse1) || !aligned4(lse2))
         return STREAMKL_ERR_UNSUPPORTED;
     skl::PagedParams p = {};
-    if ((rc = paged_params(cache1, table, width, lengths, B, Hq, NQ, scale, causal, workspace, workspace_bytes, &p)))
+    if ((rc = paged_params(cache1, table, width, lengths, B, Hq, NQ, scale, causal, true, workspace, workspace_bytes, &p)))
         return rc;
     p.a = {static_cast<const uint8_t*>(cache1->k), cache1->k_exp};
     p.b = {static_cast<const uint8_t*>(cache2->k), cache2->k_exp};

@@ -32,7 +32,7 @@ struct KlCfg {
     static constexpr int kCtas = NT == 1 ? 3 : 2;                          // on an SM
     static constexpr int kShare = (kCtas == 3 ? 18 : 26) * 1024;           // of a warp
     static constexpr int kTiles = K1::kBytes + (SHARED ? 0 : K2::kBytes);  // one tile of each cache
-    static constexpr int H = NT <= 2 && kTiles <= 3072 ? 2 : 1;
+    static constexpr int H = kTiles <= 3072 ? 2 : 1;
     static constexpr int kKeys = H * kTileKeys;
     static constexpr int kUnit = kPagedWarps * kKeys;
     static constexpr int kStart = 4;                                   // see PagedPlan
@@ -43,10 +43,7 @@ struct KlCfg {
     static constexpr int kFit = kShare / kStage;
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kWarp = kStage * kStages;
-    static constexpr bool kSharedQ = NT > 2;
-    static constexpr int kQ = kPagedWarps * kWarp;                         // [2][NT][steps][lane]
-    static constexpr int kFactor = kQ + (kSharedQ ? 2 * NT * kSteps * 32 * 8 : 0);   // [2][NT][8]
-    static constexpr int kStats = kFactor + (kSharedQ ? 2 * NT * 8 * 4 : 0);         // [warp][5][kRows]
+    static constexpr int kStats = kPagedWarps * kWarp;                     // [warp][5][kRows]
     static constexpr int kSmem = kStats + kPagedWarps * 5 * kRows * 4;
     static constexpr int kPart = kRows * 5;
     static_assert(kStages >= 2, "ring");
@@ -70,15 +67,17 @@ __device__ __forceinline__ void kl_finish(const PagedParams& p, size_t row, cons
         p.lse1[row] = p.lse2[row] = -INFINITY;
         return;
     }
-    const float ln2 = 0.69314718056f;
-    p.lse1[row] = ln2 * (a[0] + log2f(a[1]));
-    p.lse2[row] = ln2 * (a[2] + log2f(a[3]));
-    p.kl[row] = (float)((double)ln2 * ((double)(a[4] / a[1]) + ((double)a[2] - (double)a[0]) + (double)log2f(a[3] / a[1])));
+    const double ln2 = 0.693147180559945309417;
+    p.lse1[row] = (float)ln2 * (a[0] + log2f(a[1]));
+    p.lse2[row] = (float)ln2 * (a[2] + log2f(a[3]));
+    p.kl[row] = (float)(ln2 * ((double)(a[4] / a[1]) + ((double)a[2] - (double)a[0]) + (double)log2f(a[3] / a[1])));
 }
 
-// S^T of one tile: c[nt] += K Q^T for every block of 8 query rows.  at: the lane's load offsets.
-template <int D, bool F8, int NT, bool SHARED_Q>
-__device__ __forceinline__ void tile_scores(uint32_t ks, const uint32_t* at, int lane, const uint2* qf, uint32_t qs, float (*c)[4]) {
+// S^T of one tile: c[nt] += K Q^T for every block of 8 query rows; BOTH: also c2 from qf2 with the same keys.
+// at: the lane's load offsets.
+template <int D, bool F8, int NT, bool BOTH>
+__device__ __forceinline__ void tile_scores(uint32_t ks, const uint32_t* at, const uint2* qf, float (*c)[4], const uint2* qf2,
+                                            float (*c2)[4]) {
     using K = KeyTile<D, F8>;
     constexpr int kSteps = D / 16;
 #pragma unroll
@@ -100,9 +99,12 @@ __device__ __forceinline__ void tile_scores(uint32_t ks, const uint32_t* at, int
             const int step = u * K::kSteps + w;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q = SHARED_Q ? lds64(qs + ((nt * kSteps + step) * 32 + lane) * 8)
-                                         : qf[SHARED_Q ? 0 : nt * kSteps + step];
+                const uint2 q = qf[nt * kSteps + step];
                 mma16816<F8>(c[nt], a0, a1, a2, a3, q.x, q.y);
+                if (BOTH) {
+                    const uint2 r = qf2[nt * kSteps + step];
+                    mma16816<F8>(c2[nt], a0, a1, a2, a3, r.x, r.y);
+                }
             }
         }
     }
@@ -133,13 +135,12 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         const size_t qrow = ((size_t)walk.b * p.Hkv + h) * p.rows;
         const int* table = p.table + (size_t)walk.b * p.width;
         const int key00 = walk.u0 * C::kUnit + warp * C::kKeys;
-        Queries<D, F1> raw1[C::kSharedQ ? 1 : NT];
-        Queries<D, F2> raw2[C::kSharedQ ? 1 : NT];
+        Queries<D, F1> raw1[NT];
+        Queries<D, F2> raw2[NT];
 #pragma unroll
-        for (int nt = 0; nt < (C::kSharedQ ? 1 : NT); ++nt) {
-            const int at = row0 + 8 * (C::kSharedQ ? warp : nt);
-            raw1[nt].load(p.q1 + qrow * D, at, p.rows);
-            raw2[nt].load(p.q2 + qrow * D, at, p.rows);
+        for (int nt = 0; nt < NT; ++nt) {
+            raw1[nt].load(p.q1 + qrow * D, row0 + 8 * nt, p.rows);
+            raw2[nt].load(p.q2 + qrow * D, row0 + 8 * nt, p.rows);
         }
         uint32_t bad = 0;         // bit (turn % 16) * 2 + tile: no such page
         PageAhead<H> pages;
@@ -169,41 +170,15 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) request(i, ring + i * C::kStage);
 
-        uint2 qf1[C::kSharedQ ? 1 : NT * C::kSteps], qf2[C::kSharedQ ? 1 : NT * C::kSteps];
-        float fac1[NT][2], fac2[NT][2];
-        if (C::kSharedQ) {
-            uint2 f[C::kSteps];
-            float* fs = reinterpret_cast<float*>(smem + C::kFactor);
-            uint2* qs = reinterpret_cast<uint2*>(smem + C::kQ);
-            float one = raw1[0].fragments(p.sl2, f);
-            if (warp < NT) {
+        uint2 qf1[NT * C::kSteps], qf2[NT * C::kSteps];
+        float fac1[NT][2], fac2[NT][2];       // of query 2t + j
 #pragma unroll
-                for (int s = 0; s < C::kSteps; ++s) qs[(warp * C::kSteps + s) * 32 + lane] = f[s];
-                if (t == 0) fs[warp * 8 + g] = one;
-            }
-            one = raw2[0].fragments(p.sl2, f);
-            if (warp < NT) {
+        for (int nt = 0; nt < NT; ++nt) {
+            const float f1 = raw1[nt].fragments(p.sl2, qf1 + nt * C::kSteps), f2 = raw2[nt].fragments(p.sl2, qf2 + nt * C::kSteps);
 #pragma unroll
-                for (int s = 0; s < C::kSteps; ++s) qs[((NT + warp) * C::kSteps + s) * 32 + lane] = f[s];
-                if (t == 0) fs[(NT + warp) * 8 + g] = one;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    fac1[nt][j] = fs[nt * 8 + 2 * t + j];
-                    fac2[nt][j] = fs[(NT + nt) * 8 + 2 * t + j];
-                }
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float one = raw1[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf1 + (C::kSharedQ ? 0 : nt * C::kSteps));
-                fac1[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
-                fac1[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
-                one = raw2[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf2 + (C::kSharedQ ? 0 : nt * C::kSteps));
-                fac2[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
-                fac2[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
+            for (int j = 0; j < 2; ++j) {
+                fac1[nt][j] = __shfl_sync(0xffffffffu, f1, 8 * t + 4 * j);
+                fac2[nt][j] = __shfl_sync(0xffffffffu, f2, 8 * t + 4 * j);
             }
         }
         // first key that a row does not see (of query 2t + j of block nt); the least over all rows
@@ -240,9 +215,8 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) s1[nt][c] = s2[nt][c] = 0.f;
-                tile_scores<D, F1, NT, C::kSharedQ>(ks + x * K1::kBytes, at1, lane, qf1, sb + C::kQ, s1);
-                tile_scores<D, F2, NT, C::kSharedQ>(SHARED ? ks + x * K1::kBytes : ks + C::kOff2 + x * K2::kBytes, at2, lane, qf2,
-                                                    sb + C::kQ + NT * C::kSteps * 256, s2);
+                tile_scores<D, F1, NT, SHARED>(ks + x * K1::kBytes, at1, qf1, s1, qf2, s2);
+                if (!SHARED) tile_scores<D, F2, NT, false>(ks + C::kOff2 + x * K2::kBytes, at2, qf2, s2, nullptr, nullptr);
                 float k1[2] = {1.f, 1.f}, k2[2] = {1.f, 1.f};
                 if (F1) {
                     k1[0] = exp_scale(lds8(ks + C::kExp1 + x * 16 + g));
@@ -367,7 +341,7 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
             const int c0 = walk.c0(), c1 = walk.c1();
             if (arrive_last(p.arrived + c0, c1 - c0 + 1, reinterpret_cast<int*>(smem))) {
                 // a power of two of lanes to a row, every such state each
-                constexpr int kLanes = NT == 1 ? 16 : NT == 2 ? 8 : 4;
+                constexpr int kLanes = NT == 1 ? 16 : 8;
                 const int jr = threadIdx.x / kLanes, sub = threadIdx.x % kLanes, first_slot = walk.first_slot();
                 float x[5] = {kNoMax, 0.f, kNoMax, 0.f, 0.f}, y[5];
                 if (jr < rows) {
