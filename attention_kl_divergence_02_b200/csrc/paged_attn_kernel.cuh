@@ -79,18 +79,21 @@ struct ValueTile : RowTile<D, F8> {
     }
 };
 
-// NT: blocks of 8 query rows; a warp folds H 16-key tiles at a time.  Two tiles halve the shuffles,
-// rescalings and waits per key and give the products two independent chains; for more than 16 rows the
-// registers do not hold them.
+// NT: blocks of 8 query rows; a warp folds H 16-key tiles at a time.  Two tiles halve the waits and the
+// bookkeeping per key and give the products two independent chains (20 rows over e4m3 keys: 38.4 us with
+// one, 36.2 with two); the registers do not hold them with 32 rows, nor a warp's shared memory three
+// slots of them with bf16 rows of d = 128 (and 168 us are near the floor of 164 there).
 template <int D, bool F8, int NT>
 struct AttnCfg {
     using K = KeyTile<D, F8>;
     using V = ValueTile<D, F8>;
     static constexpr int H = NT == 4 || (NT == 3 && !F8) || (D == 128 && !F8) ? 1 : 2;
-    static constexpr int kCtas = NT == 1 ? 3 : 2;                      // on an SM
+    // Resident CTAs per SM, registers permitting.  At most 8 rows, 131072 bf16 keys of 16 heads / 64 uneven e4m3
+    // sequences: 2: 170 / 125 us, 3: 169 / 109, 4 (128 registers, spills): 178 / 108.
+    static constexpr int kCtas = NT == 1 ? 3 : 2;
     static constexpr int kKeys = H * kTileKeys;                        // of a warp at a time
     static constexpr int kUnit = kPagedWarps * kKeys;
-    static constexpr int kStart = NT == 1 ? 4 : 6;                                   // see PagedPlan
+    static constexpr int kStart = NT == 1 ? 4 : 6;                     // see PagedPlan
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;
     // A slot holds the keys or the values of kKeys tokens, and their exponents.  The slots form a ring,

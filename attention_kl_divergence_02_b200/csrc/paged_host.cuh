@@ -4,7 +4,7 @@
 
 namespace {
 
-constexpr int kWholeUnits = 8;
+constexpr int kWholeFew = 3, kWholeMany = 8;      // units
 constexpr int kJoinApart = 256;      // states * rows of a segment beyond which the join is a kernel of its own
 constexpr int kPagedMaxCtas = 4;     // most resident CTAs per SM of any variant
 
@@ -16,7 +16,8 @@ int page_shift_of(int n) {
 
 // Query rows are folded in blocks of 8 n.  Attention: n = 1 to 4, the fewest blocks that hold a KV head's rows.
 // Divergence: 1 or 2; more rows are several blocks, which read the keys again, from L2, since the CTAs
-// that do the blocks of one head run side by side (FIGURE2).
+// that do the blocks of one head run side by side (32 rows over 64 x 8192 bf16 keys of d = 128: 52 us, and
+// 65 with one block of 32, whose query fragments do not fit the registers).
 int paged_row_tiles(long long rows, bool divergence) {
     const int most = divergence ? 2 : 4;
     return (int)std::min<long long>((rows + 7) / 8, most);
@@ -52,14 +53,18 @@ int launch_main(K kernel, int smem, const skl::PagedParams& p, cudaStream_t st, 
     }
 }
 
-// The grid, and whether segments are dealt out whole: where no segment has more than kWholeUnits units.
-// (One sequence of 300 keys, 8 KV heads, d = 128: FIGURE.)
+// The grid, and whether segments are dealt out whole instead of in equal shares: where all are short, since a
+// whole segment needs no plan, partial state or join.  Measured, 8 KV heads, d = 128, attention over
+// bf16 (e4m3), whole against shares, us: one sequence of 128 keys 4.1 against 5.8, 256 keys 5.4 against 5.9
+// (5.9 against 7.1), 512 keys 8.1 against 6.3 (8.1 against 7.1); 32 sequences of 512 keys 14.0 against 17.1
+// (9.7 against 12.7).  Units are 64 (128) keys.  With enough segments to fill half the grid, eight units
+// bound what uneven lengths can cost.
 template <int UNIT>
 void paged_grid(skl::PagedParams* p, int ctas) {
     const long long units = ((long long)p->width * p->page_size + UNIT - 1) / UNIT;
     const long long segments = (long long)p->B * p->Hkv * p->rblocks;
     p->grid = ctas * paged_sms();
-    p->whole = units <= kWholeUnits ? 1 : 0;
+    p->whole = units <= (2 * segments >= p->grid ? kWholeMany : kWholeFew) ? 1 : 0;
     if (p->whole) p->grid = (int)std::min<long long>(p->grid, segments);
 }
 

@@ -138,7 +138,14 @@ ATTN = [
     (6, 2, 5, 128, 16, "bf16", True, [40, 4, 0, 2000]),        # 15 rows
     (8, 1, 4, 128, 16, "bf16", True, [100, 31, 1601]),         # 32 rows
     (1, 1, 33, 64, 1024, "bf16", True, [10, 33, 1025]),
-    (3, 1, 1, 64, 16, "e4m3", True, list(range(200))),         # more sequences than threads
+    (3, 1, 1, 64, 16, "e4m3", True, list(range(200))),         # many sequences, each whole
+    (4, 2, 1, 64, 16, "bf16", True, [37 * i % 1500 for i in range(70)]),   # many, in shares
+    (8, 1, 2, 128, 16, "e4m3", True, [513, 1, 130]),           # 16 rows
+    (8, 1, 3, 128, 32, "bf16", True, [513, 2, 130]),           # 24 rows
+    (8, 1, 4, 64, 32, "e4m3", True, [900, 3, 131]),            # 32 rows
+    (8, 1, 4, 128, 32, "e4m3", False, [900, 3, 131]),
+    (16, 16, 1, 64, 1024, "e4m3", True, [65600]),              # more turns than a batch of page entries
+    (16, 16, 1, 128, 1024, "bf16", True, [62001]),
 ]
 
 
@@ -300,6 +307,10 @@ KL = [
     (14, 2, 5, 128, 32, "e4m3", "bf16", True, [40, 4, 3000]),
     (8, 1, 4, 128, 16, "bf16", "same", True, [100, 31, 1601]),
     (3, 1, 1, 64, 16, "bf16", "e4m3", True, list(range(200))),
+    (4, 2, 1, 64, 16, "bf16", "same", True, [37 * i % 1500 for i in range(70)]),
+    (8, 1, 5, 128, 32, "bf16", "bf16", True, [900, 3, 131]),   # 40 rows: blocks of 16
+    (16, 16, 1, 64, 1024, "e4m3", "bf16", True, [65600]),
+    (16, 16, 1, 128, 1024, "bf16", "same", True, [62001]),
 ]
 
 
@@ -462,3 +473,103 @@ def test_on_another_stream():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert not bool(kl[0].any()) and float((kl[1] - want[1]).abs().max()) <= 1e-5
         assert torch.equal(back[0][1, :, :33], c.k[1])
+
+
+def test_two_streams_at_once():
+    """Two calls that overlap, each with its own workspace."""
+    c = ref.Case([9000, 300, 4000], 4, 128, 64, "e4m3", seed=81)
+    q = [ref.queries(3, 8, 1, 128, seed=82 + i) for i in range(2)]
+    want = [binding.paged_attn(x, c.cache, c.table, c.len) for x in q]
+    spaces = [workspace(3, 8, 4, 1, 128) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = binding.paged_attn(q[i], c.cache, c.table, c.len, workspace=spaces[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+        assert counters_are_zero(spaces[i])
+
+
+def test_sequences_share_pages():
+    """Two sequences with a common prefix of pages, one twice in the batch."""
+    c = ref.Case([200, 200, 90], 2, 64, 16, "bf16", seed=91)
+    table = c.table.clone()
+    table[1] = table[0]                       # the same 200 keys
+    table[2, :3] = table[0, :3]               # 48 keys of the first, then its own
+    c.kc[1], c.vc[1] = c.kc[0], c.vc[0]
+    for pool in (c.kc, c.vc):
+        pool[2] = torch.cat([pool[0][:, :48], pool[2][:, 48:]], 1)
+    q = ref.queries(3, 4, 1, 64, seed=92)
+    out, lse = binding.paged_attn(q, c.cache, table, c.len)
+    want, want_lse, tol, tol_lse = ref.attention(c, q, 0.125, True)
+    ref.close(out, want, tol, "out")
+    ref.close(lse, want_lse, tol_lse, "lse")
+
+
+def test_one_workspace_for_calls_of_any_size():
+    big = workspace(8, 64, 2, 1, 128)
+    for Hq, Hkv, d, lengths, seed in ((64, 2, 128, [3000] * 8, 1), (2, 2, 64, [5000], 2), (8, 2, 128, [700, 64], 3),
+                                      (64, 2, 128, [3000] * 8, 1)):
+        c = ref.Case(lengths, Hkv, d, 64, "bf16", seed=100 + seed)
+        q = ref.queries(len(lengths), Hq, 1, d, seed=110 + seed)
+        own = binding.paged_attn(q, c.cache, c.table, c.len)
+        got = binding.paged_attn(q, c.cache, c.table, c.len, workspace=big)
+        kl = binding.paged_kl(q, c.cache, q, c.cache, c.table, c.len, workspace=big)
+        assert torch.equal(got[0], own[0]) and torch.equal(got[1], own[1]) and not bool(kl[0].any())
+        assert counters_are_zero(big)
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_refusals(fast, monkeypatch):
+    """Tensors that the kernels would misread, by the extension's path and by the plain one."""
+    if not fast:
+        monkeypatch.setattr(binding, "_fast", None)
+    c = ref.Case([40, 20], 2, 64, 16, "bf16", seed=120)
+    q = ref.queries(2, 4, 1, 64, seed=121)
+    ws = workspace(2, 4, 2, 1, 64)
+    new = torch.zeros((2, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    want = binding.paged_attn(q, c.cache, c.table, c.len)
+    got = binding.paged_attn(q, c.cache, c.table, c.len, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for bad in (q.float(), q[:1], q[..., :32], q.transpose(1, 2), q[:, :3].contiguous(), q.cpu(), q[0]):
+        with pytest.raises(ValueError):
+            binding.paged_attn(bad, c.cache, c.table, c.len, workspace=ws)
+        with pytest.raises(ValueError):
+            binding.paged_kl(q, c.cache, bad, c.cache, c.table, c.len, workspace=ws)
+    for table in (c.table.long(), c.table[:1], c.table.t().contiguous().t(), c.table[0], c.table.cpu()):
+        with pytest.raises(ValueError):
+            binding.paged_attn(q, c.cache, table, c.len, workspace=ws)
+        with pytest.raises(ValueError):
+            binding.cache_append(c.cache, new, new, table, zero)
+        with pytest.raises(ValueError):
+            binding.cache_gather(c.cache, table, c.len, out=(new, new))
+    for lengths in (c.len.long(), c.len[:1], c.len.cpu()):
+        with pytest.raises(ValueError):
+            binding.paged_attn(q, c.cache, c.table, lengths, workspace=ws)
+        with pytest.raises(ValueError):
+            binding.cache_append(c.cache, new, new, c.table, lengths)
+    for space in (ws[::2], ws.half(), ws.cpu()):
+        with pytest.raises(ValueError):
+            binding.paged_attn(q, c.cache, c.table, c.len, workspace=space)
+    with pytest.raises(binding.StreamKLError):        # too small: the library's own check
+        binding.paged_attn(q, c.cache, c.table, c.len, workspace=ws[:64].contiguous())
+    with pytest.raises(binding.StreamKLError):
+        binding.paged_attn(q, c.cache, c.table, c.len, scale=-1.0, workspace=ws)
+    for rows_ in (new[:, :1].contiguous(), new.float(), new[..., :32].contiguous(), new.transpose(2, 3)):
+        with pytest.raises(ValueError):
+            binding.cache_append(c.cache, rows_, rows_, c.table, zero)
+    keys = binding.PagedCache(c.cache.k)
+    with pytest.raises(ValueError):
+        binding.paged_attn(q, keys, c.table, c.len, workspace=ws)
+    with pytest.raises(ValueError):
+        binding.cache_append(keys, new, new, c.table, zero)
+    kl = binding.paged_kl(q, keys, q, keys, c.table, c.len, workspace=ws)
+    assert not bool(kl[0].any()) and status() == binding.OK
+    other = binding.PagedCache.empty(c.pages + 1, 2, 16, 64)
+    with pytest.raises((ValueError, binding.StreamKLError)):
+        binding.paged_kl(q, c.cache, q, other, c.table, c.len, workspace=ws)

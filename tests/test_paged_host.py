@@ -157,3 +157,30 @@ def test_python_calls_refuse_host_tensors():
         binding.PagedCache(k)
     with pytest.raises(ValueError):
         binding.PagedCache(k.float())
+
+
+def test_the_extension_leaves_everything_odd_to_python():
+    """csrc/fastcall.c answers NotImplemented, without an exception, for whatever is not its everyday case."""
+    binding._start()
+    if binding._fast is None:
+        pytest.skip("the extension is not built (no Python headers)")
+    struct = cache(type=binding.CACHE_BF16)
+    at = ctypes.addressof(struct)
+    q = torch.zeros((2, 4, 1, 64), dtype=torch.bfloat16)
+    table, n = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(4096)
+    new = torch.zeros((2, 2, 3, 64), dtype=torch.bfloat16)
+    for args in ((q, at, 0, table, n, 0.1, True, ws),              # tensors on the host
+                 (q, at, 0, table, n, 0.1, True, None),
+                 (None, at, 0, table, n, 0.1, True, ws),
+                 (q, 0, 0, table, n, 0.1, True, ws),
+                 (q, "x", 0, table, n, 0.1, True, ws),
+                 (q, at, 0, 7, n, 0.1, True, ws),
+                 (q, at, 0, table, n, "x", True, ws),
+                 (q,)):
+        assert binding._fast.attn(*args) is NotImplemented
+    assert binding._fast.kl(q, at, q, at, 0, table, n, 0.1, True, ws) is NotImplemented
+    assert binding._fast.kl(q, at, object(), at, 0, table, n, 0.1, True, ws) is NotImplemented
+    for append in (True, False):
+        assert binding._fast.move(at, 0, append, new, new, table, n, n) is NotImplemented
+        assert binding._fast.move(at, 0, append, new, None, table, None, None) is NotImplemented
