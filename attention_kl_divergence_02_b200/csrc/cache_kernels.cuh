@@ -8,24 +8,29 @@
 // mantissa.  2^-96 keeps scale, inverse and every code's value normal in fp32 and bf16.
 // Reading back is exact: 4 significant bits fit bf16.
 //
-// Bound: memory.  A row takes d / 8 lanes with 16 bytes of bf16 each; of a warp's 2 (d = 128) or 4
-// (d = 64) rows at a time, one half are keys and the other half the same tokens' values, so the pool
-// rows are looked up once for both, by one lane per token, before the loads.  A warp does
-// kCacheTurns such turns, all of whose loads are in flight together.
+// Bound: memory.  Of the rows that a warp holds at a time, one half are keys and the other half the same
+// tokens' values, so the pool rows are looked up once for both, by one lane per token, before the loads; a warp
+// does kCacheTurns such turns, all of whose loads are in flight together.  A lane takes 16 contiguous
+// bytes of the side that is written: 16 elements of a row to be quantised, 8 of one to be read back
+// (there, 16 elements would be two stores of half a sector each: 81 us instead of 70 for 32 heads of
+// 16384 rows of d = 128; quantising them takes 64, 96 % of measured HBM).
 #pragma once
 
 #include "paged.cuh"
 
 namespace skl {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 128;
 constexpr int kCacheTurns = 4;
 
-template <int D>
+template <int D, int ELEMS>
 struct CacheCfg {
-    static constexpr int kLanes = D / 8;                  // of a row
+    static constexpr int kElems = ELEMS;                  // of a lane
+    static constexpr int kLoads = kElems / 8;             // 16-byte loads of its dense part
+    static constexpr int kLanes = D / kElems;             // of a row
     static constexpr int kGroups = 32 / kLanes;           // rows at a time
     static constexpr int kTokens = kGroups / 2 * kCacheTurns;   // of a warp
+    static_assert(kLanes >= kCacheTurns, "a row's lanes keep the exponents of their turns");
 };
 
 struct CacheParams {
@@ -77,58 +82,76 @@ __device__ __forceinline__ uint32_t top_bits(uint32_t x) {
     return max(lo, hi);
 }
 
+template <bool FINITE>
+__device__ __forceinline__ uint32_t top_bits4(uint4 x) {
+    return max(max(top_bits<FINITE>(x.x), top_bits<FINITE>(x.y)), max(top_bits<FINITE>(x.z), top_bits<FINITE>(x.w)));
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_append_kernel(const CacheParams p) {
-    using C = CacheCfg<D>;
+    using C = CacheCfg<D, F8 ? 16 : 8>;
     const int lane = threadIdx.x & 31, c = lane % C::kLanes, pool = (lane / C::kLanes) & 1, sub = lane / C::kLanes / 2;
     const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
     const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
     if (bh >= p.B * p.Hkv) return;
     const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
-    const uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * 8;
+    const uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * C::kElems;
     uint8_t* rows = pool ? p.rows[1] : p.rows[0];
     int row[kCacheTurns];
-    uint4 x[kCacheTurns];
+    uint4 x[kCacheTurns][C::kLoads];
 #pragma unroll
     for (int r = 0; r < kCacheTurns; ++r) {
         const int i = r * (C::kGroups / 2) + sub;
         row[r] = __shfl_sync(0xffffffffu, mine, i);
-        x[r] = make_uint4(0, 0, 0, 0);
-        if (row[r] >= 0) x[r] = __ldg(reinterpret_cast<const uint4*>(dense + (size_t)i * D));
+#pragma unroll
+        for (int k = 0; k < C::kLoads; ++k) {
+            x[r][k] = make_uint4(0, 0, 0, 0);
+            if (row[r] >= 0) x[r][k] = __ldg(reinterpret_cast<const uint4*>(dense + (size_t)i * D) + k);
+        }
     }
     if (!F8) {
 #pragma unroll
         for (int r = 0; r < kCacheTurns; ++r)
-            if (row[r] >= 0) *reinterpret_cast<uint4*>(rows + (size_t)row[r] * D * 2 + c * 16) = x[r];
+            if (row[r] >= 0) *reinterpret_cast<uint4*>(rows + (size_t)row[r] * D * 2 + c * 16) = x[r][0];
         return;
     }
-    uint32_t exponent = 0;                                // lane c < 8 keeps that of turn c
+    uint32_t exponent = 0;                                // lane c keeps that of turn c
     int exponent_row = -1;
 #pragma unroll
     for (int r = 0; r < kCacheTurns; ++r) {
-        uint32_t top = max(max(top_bits<false>(x[r].x), top_bits<false>(x[r].y)), max(top_bits<false>(x[r].z), top_bits<false>(x[r].w)));
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < C::kLoads; ++k) top = max(top, top_bits4<false>(x[r][k]));
 #pragma unroll
         for (int d = C::kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         if (__any_sync(0xffffffffu, top >= 0x7f80u)) {
-            top = max(max(top_bits<true>(x[r].x), top_bits<true>(x[r].y)), max(top_bits<true>(x[r].z), top_bits<true>(x[r].w)));
+            top = 0;
+#pragma unroll
+            for (int k = 0; k < C::kLoads; ++k) top = max(top, top_bits4<true>(x[r][k]));
 #pragma unroll
             for (int d = C::kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         }
         const uint32_t e = row_exponent(top);
         const float inv = exp_scale(254u - e);            // 2^-(e - 127)
-        const uint32_t v[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-        uint32_t y[4];
+        uint32_t y[2 * C::kLoads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float lo = bf16_lo(v[k]) * inv, hi = bf16_hi(v[k]) * inv;
-            if (e == 247) {          // 256 * 2^120 would be infinite: the last scale ends at 240
-                if (fabsf(lo) > 240.f) lo = copysignf(240.f, lo);
-                if (fabsf(hi) > 240.f) hi = copysignf(240.f, hi);
+        for (int k = 0; k < C::kLoads; ++k) {
+            const uint32_t v[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo = bf16_lo(v[i]) * inv, hi = bf16_hi(v[i]) * inv;
+                if (e == 247) {          // 256 * 2^120 would be infinite: the last scale ends at 240
+                    if (fabsf(lo) > 240.f) lo = copysignf(240.f, lo);
+                    if (fabsf(hi) > 240.f) hi = copysignf(240.f, hi);
+                }
+                z[i] = e4m3x2(lo, hi);
             }
-            y[k] = e4m3x2(lo, hi);
+            y[2 * k] = z[0] | z[1] << 16;
+            y[2 * k + 1] = z[2] | z[3] << 16;
         }
-        if (row[r] >= 0) *reinterpret_cast<uint2*>(rows + (size_t)row[r] * D + c * 8) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+        if (row[r] >= 0) *reinterpret_cast<uint4*>(rows + (size_t)row[r] * D + c * 16) = make_uint4(y[0], y[1], y[C::kLoads], y[2 * C::kLoads - 1]);
         if (c == r) {
             exponent = e;
             exponent_row = row[r];
@@ -139,14 +162,14 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_append_kernel(co
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_gather_kernel(const CacheParams p) {
-    using C = CacheCfg<D>;
+    using C = CacheCfg<D, 8>;
     const int lane = threadIdx.x & 31, c = lane % C::kLanes, pool = (lane / C::kLanes) & 1, sub = lane / C::kLanes / 2;
     const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
     const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
     if (bh >= p.B * p.Hkv) return;
     const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
-    uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * 8;
+    uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * C::kElems;
     const uint8_t* rows = pool ? p.rows[1] : p.rows[0];
     int row[kCacheTurns];
     uint4 x[kCacheTurns];
@@ -154,6 +177,7 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_gather_kernel(co
 #pragma unroll
     for (int r = 0; r < kCacheTurns; ++r) {
         row[r] = __shfl_sync(0xffffffffu, mine, r * (C::kGroups / 2) + sub);
+        x[r] = make_uint4(0, 0, 0, 0);
         if (row[r] < 0) continue;
         if (F8) {
             const uint2 v = *reinterpret_cast<const uint2*>(rows + (size_t)row[r] * D + c * 8);

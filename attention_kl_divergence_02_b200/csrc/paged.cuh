@@ -126,6 +126,7 @@ struct PagedWalk {
     int pos, base, end, first, share;  // position on the line, where the sequence begins, end and begin of the share
 
     __device__ __forceinline__ bool start(const PagedParams& p) {
+        first = 0;
         if (p.whole) {
             pos = (int)blockIdx.x;
             end = p.B * p.Hkv * p.rblocks;
@@ -154,7 +155,8 @@ struct PagedWalk {
             if (seg + 1 == p.Hkv * p.rblocks) {
                 base = pos;
                 do {
-                    len = seq_len(p, ++b);
+                    if (++b >= p.B) return false;      // not met while the lengths stay as they are
+                    len = seq_len(p, b);
                 } while (len == 0);
                 units = Plan::units(len);
             }

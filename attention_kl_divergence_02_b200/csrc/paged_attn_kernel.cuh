@@ -637,7 +637,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         }
                     } else {
 #pragma unroll 1
-                        for (int i0 = 0; i0 < p.NQ; ++i0) {
+                        for (int y = 0; y < min(p.NQ, C::kRows); ++y) {
+                            const int i0 = (row0 + y) % p.NQ;      // the positions of this block's rows
                             uint32_t mask[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) mask[j] = keyx + V::key(j, t) < least + i0 ? ~0u : 0u;

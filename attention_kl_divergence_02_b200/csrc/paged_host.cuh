@@ -108,12 +108,14 @@ int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, co
     p.B = B; p.Hkv = c->Hkv; p.NT = NT; p.width = width; p.pages = c->pages;
     p.page_size = c->page_size;
     p.page_shift = page_shift_of(c->page_size);
-    const int tokens = c->d == 128 ? skl::CacheCfg<128>::kTokens : skl::CacheCfg<64>::kTokens;
+    const bool f8 = c->type == STREAMKL_CACHE_E4M3;
+    // an append to an e4m3 cache takes 16 elements a lane, everything else 8
+    const int tokens = c->d == 128 ? (append && f8 ? skl::CacheCfg<128, 16>::kTokens : skl::CacheCfg<128, 8>::kTokens)
+                                   : (append && f8 ? skl::CacheCfg<64, 16>::kTokens : skl::CacheCfg<64, 8>::kTokens);
     const long long warps = (long long)B * c->Hkv * ((NT + tokens - 1) / tokens);
     const int per = skl::kCacheThreads / 32;
     const int grid = (int)((warps + per - 1) / per);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool f8 = c->type == STREAMKL_CACHE_E4M3;
     auto kernel = c->d == 128 ? (f8 ? (append ? skl::streamkl_cache_append_kernel<128, true> : skl::streamkl_cache_gather_kernel<128, true>)
                                     : (append ? skl::streamkl_cache_append_kernel<128, false> : skl::streamkl_cache_gather_kernel<128, false>))
                               : (f8 ? (append ? skl::streamkl_cache_append_kernel<64, true> : skl::streamkl_cache_gather_kernel<64, true>)

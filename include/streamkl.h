@@ -233,7 +233,8 @@ enum { STREAMKL_CACHE_BF16 = 0, STREAMKL_CACHE_E4M3 = 1 };
 typedef struct streamkl_cache {
     void* k;          /* [pages, Hkv, page_size, d], bf16 or e4m3 */
     void* v;          /* the same; not used (may be NULL) in streamkl_paged_kl */
-    uint8_t* k_exp;   /* e4m3: [pages, Hkv, page_size], a row's scale is 2^(byte - 127) */
+    uint8_t* k_exp;   /* e4m3: [pages, Hkv, page_size], a row's scale is 2^(byte - 127),
+                         byte 1 to 254 */
     uint8_t* v_exp;   /*       (bf16: not used, may be NULL) */
     int type;         /* STREAMKL_CACHE_* */
     int pages;        /* pages * Hkv * page_size below 2^31 rows */

@@ -195,11 +195,12 @@ def test_attention_of_large_and_tiny_queries(kind):
     ref.close(lse, want_lse, tol_lse, "lse")
 
 
-@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_values_behind_a_rows_limit_do_not_reach_it(kind):
+@pytest.mark.parametrize("kind,NQ", [("bf16", 4), ("e4m3", 4), ("bf16", 40), ("e4m3", 40)])
+def test_values_behind_a_rows_limit_do_not_reach_it(kind, NQ):
     """The newest tokens' keys and values are NaN (bf16: and infinite): rows that do not see them keep
     their results, rows that see them are NaN."""
-    NQ, n = 4, 85                 # the limits lie inside a tile
+    n = 85                        # the limits lie inside a tile
+    blind = NQ - 2                # the rows before do not see token n - 2
     c = ref.Case([n], 2, 128, 16, kind, seed=8)
     q = ref.queries(1, 4, NQ, 128, seed=9)
     want = binding.paged_attn(q, c.cache, c.table, c.len)
@@ -213,10 +214,11 @@ def test_values_behind_a_rows_limit_do_not_reach_it(kind):
         c.cache.k.view(torch.uint8)[page, 1, slot, 5] = 0xff
     got = binding.paged_attn(q, c.cache, c.table, c.len)
     assert status() == binding.OK
-    assert torch.equal(got[0][:, :, :2], want[0][:, :, :2]) and torch.equal(got[1][:, :, :2], want[1][:, :, :2])
-    seen = got[0][:, :, 2:]
+    assert torch.equal(got[0][:, :, :blind], want[0][:, :, :blind])
+    assert torch.equal(got[1][:, :, :blind], want[1][:, :, :blind])
+    seen = got[0][:, :, blind:]
     assert not bool(torch.isfinite(seen[..., 1::3]).any()) and not bool(torch.isfinite(seen[..., ::3]).any())
-    assert bool(torch.isnan(got[1][0, 2:, 2:]).all()) and torch.equal(got[1][0, :2], want[1][0, :2])
+    assert bool(torch.isnan(got[1][0, 2:, blind:]).all()) and torch.equal(got[1][0, :2], want[1][0, :2])
 
 
 def test_pages_and_lengths_outside_the_cache():
