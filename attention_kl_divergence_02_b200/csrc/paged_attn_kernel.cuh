@@ -10,24 +10,28 @@
 // serves the loads: each warp streams its own tiles through a ring of cp.async slots that only it
 // touches (see RowTile), so no barrier of the CTA stands between a load and the next.
 //
-// Per tile a warp computes S^T = K Q^T (16 keys x 8 rows per product), takes the maxima over the
-// lanes that share a row, and turns P^T around with movmatrix into the B operand of
+// Per tile a warp computes S^T = K Q^T (16 keys x 8 rows per product), weights, and turns P^T around with movmatrix into the B operand of
 // O^T = V^T P^T (M: 16 columns of d, N: 8 rows, K: 16 keys).  V^T's fragments need two keys'
 // values of one column in a register: the lane loads the same bytes of four keys and joins them with
 // byte permutes.
 //
-// bf16 cache: P is split into two bf16 terms (hi + lo, 16 bits of it), because one bf16 rounding of P
-// (up to 2^-9 of each weight) would add as much error as the output's own rounding; the tensor pipe
-// has room for the second product.
+// bf16 cache: P is split into two bf16 terms (hi + lo, off by 2^-16 of a weight), because one bf16 rounding
+// of P (2^-8) would add as much error as the output's own rounding; the tensor pipe has room for the second
+// product.
 // e4m3 cache: values are met as fp16 (exact) without their scales 2^e_j; those go into the weights,
-// P'_j = 2^(s_j + e_j - m'), with a running maximum m' of s_j + e_j, so that P' <= 1 whatever the
-// scales are; fp16 keeps 11 bits of it (error 2^-12), which is below the output's rounding.  l keeps its
-// own maximum m of s_j.
+// P'_j = 2^(s_j + e_j - m'), with a running maximum m' of s_j + e_j, so that P' stays within fp16 whatever
+// the scales are; its rounding (2^-11) is an eighth of the output's.  l keeps its own maximum m of s_j.  Where a turn's scales lie within 2^kNear of each other (and all so far within
+// 2^-40 .. 2^40), P' is the sum's weight times two factors and m' moves by the bound max s + max e,
+// which is at most kNear too high; elsewhere both are taken key by key, with a second exponential.  Too high
+// a reference costs the smallest weights bits below fp16's 2^-24: 2^-25 of the largest weight without,
+// 2^-21 at worst with the bound.
 #pragma once
 
 #include "paged.cuh"
 
 namespace skl {
+
+constexpr int kNear = 4;      // octaves, see above
 
 // Values: lane (g, t) of V^T's fragments holds columns of keys 2t, 2t + 1, 2t + 8 and 2t + 9, and takes
 // kElems contiguous ones of each: chunk g (and g + 8 where a row has 16), or half a chunk where it has
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     e_max = (int)__reduce_max_sync(0xffffffffu, in ? e : 0u);
                     const int e_min = (int)__reduce_min_sync(0xffffffffu, in ? e : 255u);
                     tame = tame && e_min >= 127 - 40 && e_max <= 127 + 40;
-                    near = tame && e_max - e_min <= 8;
+                    near = tame && e_max - e_min <= kNear;
                     e_max -= 127;
                 }
                 // exponent byte of value key g + 8k of tile x; 127 where there is no such key

@@ -127,10 +127,12 @@ def attention(case, q, scale, causal):
             weight = 2 * e + 2.0 ** -20 + (2.0 ** -16 if case.kind == "bf16" else 2.0 ** -11) + (m / 16) * 2.0 ** -23
             tol[b, :, i] = out[b, :, i].abs() * 2.0 ** -8 + size * weight
             if case.kind != "bf16":
-                # weights below fp16's normal numbers: half its smallest step, 2^-25 of the largest p_j 2^e_j
+                # weights below fp16's normal numbers: half its smallest step, 2^-25 of the reference 2^m', and m'
+                # may be the bound max s + max e over keys whose e differ by at most 4: it exceeds the largest
+                # s_j + e_j by at most 4, so 2^-21 of the largest p_j 2^e_j for each of m codes of at most 448
                 row = v[:, :m].abs().amax(-1)
                 unit = torch.exp2(torch.ceil(torch.log2(row.clamp(min=2.0 ** -200) / 448)))
-                tol[b, :, i] += m * 2.0 ** -25 * 448 * (p * unit).amax(-1, keepdim=True)
+                tol[b, :, i] += m * 2.0 ** -21 * 448 * (p * unit).amax(-1, keepdim=True)
             tol_lse[b, :, i] = e + 2.0 ** -21 + lse[b, :, i].abs() * 2.0 ** -22
     return out, lse, tol, tol_lse
 
