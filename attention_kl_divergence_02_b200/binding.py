@@ -428,7 +428,7 @@ def bwd(mode, q1, k1, q2, k2, kl, lse1, lse2, dkl, scale=None, causal=False, out
 
 
 # ------------------------------------------------------------------ paged key-value cache
-# torch, and the extension that does the everyday case of a call (csrc/fastcall.c; None where it was not
+# torch, and the extension that does the everyday case of a call (csrc/fastcall.cpp; None where it was not
 # built), from the first PagedCache on: these calls are made once per token, and an import statement, a tuple
 # or a device object in each check adds up to the time of a kernel.
 _torch = None
@@ -444,10 +444,8 @@ def _start():
     except ImportError:
         return
     lib = load()
-    _fastcall.setup(torch.bfloat16, torch.int32, torch.float32, torch.empty_like, torch._C._cuda_getDevice,
-                    torch._C._cuda_getCurrentRawStream,
-                    *(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.streamkl_paged_attn, lib.streamkl_paged_kl,
-                                                                      lib.streamkl_cache_append, lib.streamkl_cache_gather)))
+    _fastcall.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.streamkl_paged_attn, lib.streamkl_paged_kl, lib.streamkl_cache_append, lib.streamkl_cache_gather)))
     _fast = _fastcall
 
 

@@ -14,7 +14,7 @@ LIB = os.path.join(PKG, "libstreamkl.so")
 MAIN = os.path.join(CSRC, "streamkl.cu")
 INCLUDE = os.path.join(ROOT, "include")
 FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
-FASTCALL_MAIN = os.path.join(CSRC, "fastcall.c")
+FASTCALL_MAIN = os.path.join(CSRC, "fastcall.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -54,8 +54,17 @@ def build_fastcall(force=False):
     made_of = (FASTCALL_MAIN, os.path.join(INCLUDE, "streamkl.h"))
     if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(s) <= os.path.getmtime(FASTCALL) for s in made_of):
         return FASTCALL
+    import torch
+    at = os.path.dirname(torch.__file__)
+    lib = os.path.join(at, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     tmp = FASTCALL + ".tmp.%d" % os.getpid()
-    subprocess.check_call(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", include, "-I", INCLUDE, "-o", tmp, FASTCALL_MAIN])
+    cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()), "-I", INCLUDE, "-I", include]
+    for path in (os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"), cuda):
+        cmd += ["-isystem", path]
+    cmd += ["-o", tmp, FASTCALL_MAIN, "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.check_call(cmd)
     os.replace(tmp, FASTCALL)
     return FASTCALL
 

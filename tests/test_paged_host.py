@@ -160,7 +160,7 @@ def test_python_calls_refuse_host_tensors():
 
 
 def test_the_extension_leaves_everything_odd_to_python():
-    """csrc/fastcall.c answers NotImplemented, without an exception, for whatever is not its everyday case."""
+    """csrc/fastcall.cpp answers NotImplemented, without an exception, for whatever is not its everyday case."""
     binding._start()
     if binding._fast is None:
         pytest.skip("the extension is not built (no Python headers)")
