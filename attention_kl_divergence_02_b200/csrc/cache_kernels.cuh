@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_append_kernel(co
     const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
     const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
+    wait_for_stream();
     if (bh >= p.B * p.Hkv) return;
     const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
     const uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * C::kElems;
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_gather_kernel(co
     const int groups = (p.NT + C::kTokens - 1) / C::kTokens;
     const unsigned w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int bh = w / (unsigned)groups, i0 = (w % (unsigned)groups) * C::kTokens;
+    wait_for_stream();
     if (bh >= p.B * p.Hkv) return;
     const int mine = lane < C::kTokens ? cache_row(p, bh / p.Hkv, bh % p.Hkv, i0 + lane) : -1;
     uint16_t* dense = (pool ? p.dense[1] : p.dense[0]) + ((size_t)bh * p.NT + i0) * D + c * C::kElems;

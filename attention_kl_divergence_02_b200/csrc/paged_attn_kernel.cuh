@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
     const uint32_t value_at = V::load_offset(lane);
     float* stats = reinterpret_cast<float*>(smem + C::kStats);
 
+    wait_for_stream();
     PagedWalk<C::kUnit, C::kStart> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
@@ -757,7 +758,7 @@ template <int D, int NT, int UNIT, int START>
 __global__ void __launch_bounds__(kJoinThreads) streamkl_paged_attn_join_kernel(const PagedParams p) {
     constexpr int kRows = 8 * NT, kPart = kRows * (D + 4);
     __shared__ float4 scratch[kJoinThreads / 32 * 33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");    // the main kernel is complete, its states are visible
+    wait_for_stream();      // the main kernel is complete
     PagedCut<UNIT, START> cut;
     if (!cut.find(p, blockIdx.x)) return;
     const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;

@@ -30,6 +30,24 @@ int paged_sms() { return std::min(num_sms(), kPagedMaxSms); }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// As a programmatic dependent of what ran before on the stream: see wait_for_stream.
+template <typename P>
+cudaError_t launch_after(void (*kernel)(P), dim3 grid, int threads, int smem, const P& p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) cudaGetLastError();      // it is returned here and must not meet a later check
+    return e;
+}
+
 // Launches a kernel whose shared memory needs an attribute that lasts as long as the device's context.  These
 // calls are made per token, so it is set once per kernel and device (`done`, a bit per device) and
 // again where a launch fails without it (after a cudaDeviceReset).
@@ -46,8 +64,7 @@ int launch_main(K kernel, int smem, const skl::PagedParams& p, cudaStream_t st, 
             if (rc) return rc;
             done.fetch_or(bit, std::memory_order_relaxed);
         }
-        kernel<<<p.grid, skl::kPagedThreads, smem, st>>>(p);
-        e = cudaGetLastError();
+        e = launch_after(kernel, dim3((unsigned)p.grid), skl::kPagedThreads, smem, p, st);
         if (e == cudaSuccess) return STREAMKL_OK;
         if (set) return cuda_fail(e, what);
     }
@@ -120,8 +137,7 @@ int cache_move(const streamkl_cache* c, const uint16_t* k, const uint16_t* v, co
                                     : (append ? skl::streamkl_cache_append_kernel<128, false> : skl::streamkl_cache_gather_kernel<128, false>))
                               : (f8 ? (append ? skl::streamkl_cache_append_kernel<64, true> : skl::streamkl_cache_gather_kernel<64, true>)
                                     : (append ? skl::streamkl_cache_append_kernel<64, false> : skl::streamkl_cache_gather_kernel<64, false>));
-    kernel<<<grid, skl::kCacheThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(kernel, dim3((unsigned)grid), skl::kCacheThreads, 0, p, st);
     if (e != cudaSuccess) return cuda_fail(e, append ? "streamkl_cache_append launch" : "streamkl_cache_gather launch");
     return STREAMKL_OK;
 }
@@ -175,17 +191,8 @@ int launch_paged_attn(skl::PagedParams p, cudaStream_t st) {
     if (rc || !apart) return rc;
     // where a segment has many states, each of its rows gets a CTA
     const int gy = states > 16 ? rows : NT;
-    // a programmatic dependent: its launch overlaps the main kernel's last CTAs, and it waits for them
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)gy);
-    cfg.blockDim = dim3(skl::kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit, C::kStart>, p);
+    const cudaError_t e = launch_after(skl::streamkl_paged_attn_join_kernel<D, NT, C::kUnit, C::kStart>,
+                                       dim3((unsigned)(p.grid - 1), (unsigned)gy), skl::kJoinThreads, 0, p, st);
     return e == cudaSuccess ? STREAMKL_OK : cuda_fail(e, "streamkl_paged_attn join launch");
 }
 

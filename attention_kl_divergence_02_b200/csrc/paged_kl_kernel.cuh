@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
     const uint32_t at1[2] = {(uint32_t)K1::load_offset(lane, 0), (uint32_t)K1::load_offset(lane, K1::kChunks > 1)};
     const uint32_t at2[2] = {(uint32_t)K2::load_offset(lane, 0), (uint32_t)K2::load_offset(lane, K2::kChunks > 1)};
 
+    wait_for_stream();
     PagedWalk<C::kUnit, C::kStart> walk;
     for (bool more = walk.start(p); more; more = walk.next(p)) {
         const int n = walk.n, len = walk.len;                   // units, hence turns of a warp; keys
