@@ -100,7 +100,7 @@ int check_cache(const streamkl_cache* c, bool values) {
 
 int check_table(const streamkl_cache* c, const int* table, int width, int B) {
     if (!table || width < 1 || B < 1) return STREAMKL_ERR_INVALID_ARG;
-    if ((long long)width * c->page_size >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+    if ((long long)width * c->page_size > (1ll << 30)) return STREAMKL_ERR_UNSUPPORTED;
     return STREAMKL_OK;
 }
 

@@ -223,7 +223,8 @@ int streamkl_bwd_noalloc(int mode, const uint16_t* q1, const uint16_t* k1, const
  *    counts and fp32 outputs need 4-byte alignment; every other pointer 16-byte alignment.
  *  - Several sequences may share pages for reading.  A slot that one append writes twice
  *    (the same page in two rows of the table) holds a mix of both.
- *  - Entries of a table row behind the sequence's last page are never used.  A used
+ *  - width * page_size, the most tokens of a sequence, is at most 2^30.  Entries of a table row
+ *    behind the sequence's last page are never used.  A used
  *    entry outside [0, pages) or a position or length outside [0, width * page_size] is recorded
  *    (streamkl_device_status returns STREAMKL_ERR_PAGE) and touches no memory: a length is clamped
  *    to the table, keys of such a page count as masked, such a row is neither written nor read.

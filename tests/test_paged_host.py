@@ -88,7 +88,7 @@ def test_no_cache():
     (dict(NT=0), INVALID),
     (dict(k=None), INVALID),
     (dict(v=FAKE + 2), UNSUPPORTED),
-    (dict(width=1 << 27), UNSUPPORTED),             # 2^31 tokens
+    (dict(width=(1 << 26) + 1), UNSUPPORTED),       # over 2^30 tokens
     (dict(B=1 << 20, NT=1 << 10), UNSUPPORTED),     # 2^31 rows
 ])
 def test_bad_moves(kw, want):
@@ -107,7 +107,7 @@ COMMON = [
     (dict(scale=0.0), UNSUPPORTED),
     (dict(scale=float("inf")), UNSUPPORTED),
     (dict(scale=float("nan")), UNSUPPORTED),
-    (dict(width=1 << 27), UNSUPPORTED),
+    (dict(width=(1 << 26) + 1), UNSUPPORTED),
     (dict(B=1 << 20, NQ=1 << 10), UNSUPPORTED),
     (dict(B=1 << 16, width=1 << 20), UNSUPPORTED),  # 2^35 units of keys
     (dict(ws=None), INVALID),
