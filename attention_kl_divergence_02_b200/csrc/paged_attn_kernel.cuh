@@ -140,79 +140,98 @@ __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, in
 }
 
 // Joins the partial states of CTAs c0 .. c1 (first_slot, then 2c) into rows [row, row + rows), of which
-// this is one of `shares` CTAs.  `each` of the WARPS warps take a row, every each-th state in order, kBatch
-// loaded together, and meet in shared memory (WARPS * 33 float4).
+// this is one of `shares` CTAs.  `each` of the WARPS warps take ROWS rows together, every each-th state in order,
+// kBatch loaded together, and meet in shared memory (WARPS * ROWS * 33 float4).  Two rows together where
+// there may be more than 8 keep twice the loads in flight: 7 uneven sequences, 20 rows over e4m3 keys, 34.7 -> 32.8 us,
+// 4 x 32768 keys of bf16, 32 rows, 66.1 -> 60.8; up to 8 rows have a warp or more a row anyway.
 constexpr int kBatch = 8;
 
-template <int D, int PART, int WARPS>
+struct RowState {
+    float m = kNoMax, v = kNoMax, l = 0.f;       // references of the sum and of the weighted sum, sum
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    __device__ __forceinline__ void move(float m1, float v1) {
+        const float f = ex2(v - v1);
+        l *= ex2(m - m1);
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+        m = m1;
+        v = v1;
+    }
+    // a state (m, v, l of q; x) whose references are not above this one's
+    __device__ __forceinline__ void add(float4 q, float4 x) {
+        const float f = ex2(q.y - v);
+        l = fmaf(q.z, ex2(q.x - m), l);
+        acc.x = fmaf(x.x, f, acc.x);
+        acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z);
+        acc.w = fmaf(x.w, f, acc.w);
+    }
+};
+
+template <int D, int PART, int WARPS, int ROWS>
 __device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, int first_slot, size_t row, int rows, int mine,
                                           int shares, float4* scratch) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int states = c1 - c0 + 1;
     int each = 1;
-    while (each < WARPS && (each * kBatch * 4 < states || (each * kBatch < states && each * rows < WARPS * shares))) each *= 2;
+    while (each < WARPS && (each * kBatch * 4 < states || (each * kBatch < states && each * rows < WARPS * ROWS * shares))) each *= 2;
     const int part = warp & (each - 1), group = warp / each, groups = WARPS / each;
-    for (int r0 = mine * groups; r0 < rows; r0 += shares * groups) {
-        const int r = r0 + group;
-        float M = kNoMax, MV = kNoMax, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float Mn, float Vn, float4 q, float4 x) {     // a state, references moved to Mn and Vn before
-            const float f1 = ex2(q.y - Vn);
-            L = fmaf(q.z, ex2(q.x - Mn), L);
-            acc.x = fmaf(x.x, f1, acc.x);
-            acc.y = fmaf(x.y, f1, acc.y);
-            acc.z = fmaf(x.z, f1, acc.z);
-            acc.w = fmaf(x.w, f1, acc.w);
-        };
-        auto move = [&](float Mn, float Vn) {
-            const float f0 = ex2(MV - Vn);
-            L *= ex2(M - Mn);
-            acc.x *= f0;
-            acc.y *= f0;
-            acc.z *= f0;
-            acc.w *= f0;
-            M = Mn;
-            MV = Vn;
-        };
-        if (r < rows) {
-            for (int c = c0 + part; c <= c1; c += kBatch * each) {
-                float4 q[kBatch], x[kBatch];
+    for (int r0 = mine * groups * ROWS; r0 < rows; r0 += shares * groups * ROWS) {
+        const int r = r0 + group * ROWS;
+        RowState to[ROWS];
+        for (int c = c0 + part; c <= c1 && r < rows; c += kBatch * each) {
+            float4 q[ROWS][kBatch], x[ROWS][kBatch];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int ck = c + k * each;
-                    q[k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
-                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (ck <= c1) {
-                        const float* from = p.part + (size_t)(ck == c0 ? first_slot : 2 * ck) * PART + r * (D + 4);
-                        q[k] = __ldcg(reinterpret_cast<const float4*>(from + D));
-                        x[k] = __ldcg(reinterpret_cast<const float4*>(from + 4 * (lane % (D / 4))));
+            for (int k = 0; k < kBatch; ++k) {
+                const int ck = c + k * each;
+                const float* from = p.part + (size_t)(ck == c0 ? first_slot : 2 * ck) * PART + r * (D + 4);
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    q[i][k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+                    x[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (ck <= c1 && r + i < rows) {
+                        q[i][k] = __ldcg(reinterpret_cast<const float4*>(from + i * (D + 4) + D));
+                        x[i][k] = __ldcg(reinterpret_cast<const float4*>(from + i * (D + 4) + 4 * (lane % (D / 4))));
                     }
                 }
-                float Mn = M, Vn = MV;
+            }
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                float m1 = to[i].m, v1 = to[i].v;
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    Mn = fmaxf(Mn, q[k].x);
-                    Vn = fmaxf(Vn, q[k].y);
+                    m1 = fmaxf(m1, q[i][k].x);
+                    v1 = fmaxf(v1, q[i][k].y);
                 }
-                move(Mn, Vn);
+                to[i].move(m1, v1);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) add(Mn, Vn, q[k], x[k]);
+                for (int k = 0; k < kBatch; ++k) to[i].add(q[i][k], x[i][k]);
             }
         }
         if (each > 1) {
             __syncthreads();
-            scratch[warp * 33 + lane] = acc;
-            if (lane == 0) scratch[warp * 33 + 32] = make_float4(M, MV, L, 0.f);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                scratch[(warp * ROWS + i) * 33 + lane] = to[i].acc;
+                if (lane == 0) scratch[(warp * ROWS + i) * 33 + 32] = make_float4(to[i].m, to[i].v, to[i].l, 0.f);
+            }
             __syncthreads();
             if (part == 0)
-                for (int w = warp + 1; w < warp + each; ++w) {
-                    const float4 q = scratch[w * 33 + 32], x = scratch[w * 33 + lane];
-                    const float Mn = fmaxf(M, q.x), Vn = fmaxf(MV, q.y);
-                    move(Mn, Vn);
-                    add(Mn, Vn, q, x);
-                }
+                for (int w = warp + 1; w < warp + each; ++w)
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        const float4 q = scratch[(w * ROWS + i) * 33 + 32];
+                        to[i].move(fmaxf(to[i].m, q.x), fmaxf(to[i].v, q.y));
+                        to[i].add(q, scratch[(w * ROWS + i) * 33 + lane]);
+                    }
         }
-        if (part == 0 && r < rows && lane < D / 4) attn_finish<D>(p, row + r, lane, acc, M, MV, L);
+        if (part == 0 && lane < D / 4)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+                if (r + i < rows) attn_finish<D>(p, row + r + i, lane, to[i].acc, to[i].m, to[i].v, to[i].l);
     }
 }
 
@@ -734,7 +753,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         if (!whole && p.arrived) {
             const int c0 = walk.c0(), c1 = walk.c1();
             if (arrive_last(p.arrived + c0, c1 - c0 + 1, reinterpret_cast<int*>(stats)))
-                attn_join<D, C::kPart, kPagedWarps>(p, c0, c1, walk.first_slot(), qrow + row0, rows, 0, 1, reinterpret_cast<float4*>(smem));
+                attn_join<D, C::kPart, kPagedWarps, NT == 1 ? 1 : 2>(p, c0, c1, walk.first_slot(), qrow + row0, rows, 0, 1, reinterpret_cast<float4*>(smem));
         }
         __syncthreads();
     }
@@ -763,7 +782,7 @@ __global__ void __launch_bounds__(kJoinThreads) streamkl_paged_attn_join_kernel(
     if (!cut.find(p, blockIdx.x)) return;
     const int h = cut.seg / p.rblocks, rb = cut.seg - h * p.rblocks, row0 = rb * kRows;
     const size_t qrow = ((size_t)cut.b * p.Hkv + h) * p.rows;
-    attn_join<D, kPart, kJoinThreads / 32>(p, cut.c0, cut.c1, cut.first_slot, qrow + row0, min(kRows, p.rows - row0), blockIdx.y,
+    attn_join<D, kPart, kJoinThreads / 32, 1>(p, cut.c0, cut.c1, cut.first_slot, qrow + row0, min(kRows, p.rows - row0), blockIdx.y,
                                            gridDim.y, scratch);
 }
 
