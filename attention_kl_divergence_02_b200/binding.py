@@ -543,8 +543,14 @@ def _leave(guard):
         guard.__exit__(None, None, None)
 
 
+def _given(name, t):
+    if t is None:
+        raise ValueError("%s is required" % name)
+
+
 def _need(name, t, dtype, shape, cache):
     """Refuses a tensor that the kernels would misread; `shape` is a tuple."""
+    _given(name, t)
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s on %s)"
                          % (name, dtype, shape, cache.device, t.dtype, tuple(t.shape), t.device))
@@ -552,6 +558,7 @@ def _need(name, t, dtype, shape, cache):
 
 def _width(table, B, cache):
     """Pages of a row of the table [B, width]."""
+    _given("table", table)
     shape = table.shape
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError("table must be int32 [B, width]")
@@ -561,6 +568,7 @@ def _width(table, B, cache):
 
 def _rows_shape(cache, k, v):
     """Shape of dense rows [B, Hkv, rows, d] that fit the cache."""
+    _given("k", k)
     shape = tuple(k.shape)
     if cache.v is None:
         raise ValueError("this cache has no values")
@@ -605,6 +613,7 @@ def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=No
             if rc != OK:
                 raise StreamKLError(rc, "streamkl_cache_gather")
             return out
+    _given("table", table)
     if out is None and (rows is None or rows < 1 or table.dim() != 2):
         raise ValueError("out, or rows of at least 1 and a table [B, width], are required")
     guard, handle = _enter(cache, stream)
@@ -631,6 +640,7 @@ def cache_gather(cache, table, count, start=None, rows=None, out=None, stream=No
 
 def _query_shape(name, q, cache):
     """Shape of queries [B, Hq, NQ, d] that fit the cache."""
+    _given(name, q)
     shape = tuple(q.shape)
     if len(shape) != 4 or shape[3] != cache.shape[3] or min(shape) < 1 or shape[1] % cache.shape[1]:
         raise ValueError("%s must be [B, Hq, NQ, %d], Hq a multiple of %d (got %s)"

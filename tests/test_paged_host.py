@@ -184,3 +184,18 @@ def test_the_extension_leaves_everything_odd_to_python():
     for append in (True, False):
         assert binding._fast.move(at, 0, append, new, new, table, n, n) is NotImplemented
         assert binding._fast.move(at, 0, append, new, None, table, None, None) is NotImplemented
+
+
+def test_a_missing_tensor_is_named():
+    """None in the place of a tensor meets a ValueError, as in the dense calls."""
+    class Cache:
+        v, shape, index, device = object(), (4, 2, 16, 64), 0, "cuda:0"
+    rows = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16)
+    for call in (lambda: binding.cache_append(Cache, None, rows, rows, rows, stream=0),
+                 lambda: binding.cache_gather(Cache, None, rows, rows=1, stream=0),
+                 lambda: binding._need("start", None, torch.int32, (1,), Cache),
+                 lambda: binding._width(None, 1, Cache),
+                 lambda: binding.paged_attn(None, Cache, rows, rows, stream=0),
+                 lambda: binding.paged_kl(None, Cache, rows, Cache, rows, rows, stream=0)):
+        with pytest.raises(ValueError, match="is required"):
+            call()
