@@ -12,8 +12,9 @@
 // tokens' values, so the pool rows are looked up once for both, by one lane per token, before the loads; a warp
 // does kCacheTurns such turns, all of whose loads are in flight together.  A lane takes 16 contiguous
 // bytes of the side that is written: 16 elements of a row to be quantised, 8 of one to be read back
-// (there, 16 elements would be two stores of half a sector each: 81 us instead of 70 for 32 heads of
-// 16384 rows of d = 128; quantising them takes 64, 96 % of measured HBM).
+// (there, 16 elements would be two stores of half a sector each: 81 us instead of 69 for 32 heads of
+// 16384 rows of d = 128; quantising them takes 66, 93 % of measured HBM, and 63 with read-only loads, which
+// an early launch rules out: see wait_for_stream).
 #pragma once
 
 #include "paged.cuh"
@@ -46,11 +47,11 @@ struct CacheParams {
 // The pool row of token i of sequence b, head h; -1 where there is nothing to do (behind the count)
 // or nothing that exists (recorded).
 __device__ __forceinline__ int cache_row(const CacheParams& p, int b, int h, int i) {
-    const int n = p.count ? __ldg(p.count + b) : p.NT, s = p.start ? __ldg(p.start + b) : 0;
+    const int n = p.count ? p.count[b] : p.NT, s = p.start ? p.start[b] : 0;
     if (i >= n || i >= p.NT) return -1;
     const unsigned pos = (unsigned)s + (unsigned)i;       // s, i < 2^31: no wrap for s >= 0
     if (s >= 0 && pos < (unsigned)p.width * (unsigned)p.page_size) {
-        const int page = __ldg(p.table + (size_t)b * p.width + (pos >> p.page_shift));
+        const int page = p.table[(size_t)b * p.width + (pos >> p.page_shift)];
         if ((unsigned)page < (unsigned)p.pages) return (page * p.Hkv + h) * p.page_size + (pos & (p.page_size - 1));
     }
     g_page_status = 5;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kCacheThreads) streamkl_cache_append_kernel(co
 #pragma unroll
         for (int k = 0; k < C::kLoads; ++k) {
             x[r][k] = make_uint4(0, 0, 0, 0);
-            if (row[r] >= 0) x[r][k] = __ldg(reinterpret_cast<const uint4*>(dense + (size_t)i * D) + k);
+            if (row[r] >= 0) x[r][k] = reinterpret_cast<const uint4*>(dense + (size_t)i * D)[k];
         }
     }
     if (!F8) {

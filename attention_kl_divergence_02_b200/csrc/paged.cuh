@@ -239,7 +239,9 @@ struct PagedCut {
 // Every kernel here is launched as a programmatic dependent of whatever ran before on its stream: its launch
 // overlaps that kernel's end (2.0 to 2.4 us a call between short kernels: 64 single tokens written and read
 // back 8.2 -> 5.7 us, one short sequence's attention 8.2 -> 5.8, 131072 keys 167.5 -> 165.6), and its
-// threads begin here, where they wait until that kernel is complete and its writes are visible.  Letting
+// threads begin here, where they wait until that kernel is complete and its writes are visible.  What they read
+// may have been written while they were already running, so all of it takes plain loads, behind the wait: a
+// read-only load (ld.global.nc) would promise data that is constant for the kernel's whole duration.  Letting
 // the next kernel come before this one's last CTA is done (launch_dependents) was no better: 6.0 and 7.6 us where
 // 5.8 and 5.8 are without.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -264,7 +266,7 @@ struct PageAhead {
     }
     __device__ __forceinline__ int look_up(int batch) const {
         const int at = key + batch * step;
-        return at >= 0 && at < len ? __ldg(table + (at >> shift)) : 0;
+        return at >= 0 && at < len ? table[at >> shift] : 0;
     }
     // before the first page of turn i
     __device__ __forceinline__ void turn(int i) {
@@ -440,7 +442,7 @@ struct Queries {
         for (int u = 0; u < kLoads; ++u) {
             // bf16 keys: chunk u covers columns [32u + 8t, +8); e4m3: [64(u/2) + 16t + 8(u%2), +8)
             const int col = F8 ? (u >> 1) * 64 + t * 16 + (u & 1) * 8 : u * 32 + t * 8;
-            v[u] = have ? __ldg(reinterpret_cast<const uint4*>(src + col)) : make_uint4(0, 0, 0, 0);
+            v[u] = have ? *reinterpret_cast<const uint4*>(src + col) : make_uint4(0, 0, 0, 0);
         }
     }
     // frag[s] of every k-step; returns the lane's factor by which a product is turned into a score in base 2 (of
