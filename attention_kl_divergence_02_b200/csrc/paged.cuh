@@ -445,16 +445,16 @@ struct Queries {
             v[u] = have ? *reinterpret_cast<const uint4*>(src + col) : make_uint4(0, 0, 0, 0);
         }
     }
-    // frag[s] of every k-step; returns the lane's factor by which a product is turned into a score in base 2 (of
-    // row lane / 4)
-    __device__ __forceinline__ float fragments(float sl2, uint2* frag) const {
+    // frag[s] of every k-step; returns the power of two by which the products of row lane / 4 are to be
+    // multiplied (1 for bf16 keys), beside the scale and the key's own scale
+    __device__ __forceinline__ float fragments(uint2* frag) const {
         if (!F8) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 frag[2 * u] = make_uint2(v[u].x, v[u].y);
                 frag[2 * u + 1] = make_uint2(v[u].z, v[u].w);
             }
-            return sl2;
+            return 1.f;
         }
         float top = 0.f;
 #pragma unroll
@@ -476,7 +476,7 @@ struct Queries {
             frag[2 * u] = make_uint2(h[0], h[1]);
             frag[2 * u + 1] = make_uint2(h[2], h[3]);
         }
-        return fmaxf(pow2(e) * sl2, 1.17549435e-38f);
+        return pow2(e);
     }
 };
 

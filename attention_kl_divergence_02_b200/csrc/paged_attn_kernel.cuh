@@ -3,7 +3,12 @@
 //     s_j = scale <q, k_j>,   o = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
 //
 // over the keys j that the row sees, in one pass: sum l and weighted sum o refer to a running
-// maximum m and are rescaled by 2^(m_old - m_new) when it moves (see kSlack).
+// maximum m and are rescaled by 2^(m_old - m_new) when it moves (see kSlack).  A score in base 2 is rounded once,
+// and that one value is what m is a maximum of and what m is subtracted from: were the weight's exponent
+// a fused s * factor - m of any factor, the largest key's would be its product's rounding error, 2^(E - 24) for
+// a score near 2^E, and from 2^30 on weights would all vanish or overflow.  So a bf16 cache's products are
+// multiplied by the scale first; an e4m3 cache's by scale times key scale, and what is left, the query row's
+// power of two, may be fused, because that product is exact.
 //
 // Bound: every cached byte is read once and used for 2 flops per query row and element, so with the
 // few rows of a KV head (Hq / Hkv * NQ) the floor is cache bytes / HBM bandwidth.  Everything here
@@ -21,10 +26,11 @@
 // of P (2^-8) would add as much error as the output's own rounding; the tensor pipe has room for the
 // second product.
 // e4m3 cache: values are met as fp16 (exact) without their scales 2^e_j; those go into the weights,
-// P'_j = 2^(s_j + e_j - m'), with a running maximum m' of s_j + e_j, so that P' stays within fp16 whatever
-// the scales are; its rounding (2^-11) is an eighth of the output's.  l keeps its own maximum m of s_j.
+// P'_j = 2^(s_j - m + e_j - x), where m + x follows the running maximum of s_j + e_j, so that P' stays within
+// fp16 whatever the scales are; its rounding (2^-11) is an eighth of the output's.  l keeps to m alone.  x is kept
+// instead of the sum m + x, in which scores beyond 2^24 would leave no bits for it.
 // Where a turn's scales lie within 2^kNear of each other (and all so far within 2^-40 .. 2^40), P' is
-// the sum's weight times two factors and m' moves by the bound max s + max e, which is at most kNear too
+// the sum's weight times two factors and m + x moves by the bound max s + max e, which is at most kNear too
 // high; elsewhere both are taken key by key, with a second exponential.  Too high a reference costs the
 // smallest weights bits below fp16's 2^-24: 2^-25 of the largest weight without, 2^-21 at worst with
 // the bound.
@@ -126,12 +132,13 @@ struct AttnCfg {
 };
 
 // Four columns of a finished row: o / l, rounded once to bf16, and the row's lse.  Weights that refer to
-// m' = MV come back to m = M by 2^(MV - M), after the division so that nothing overflows
-// that the result does not.  A row without keys (l = 0): zeros and -inf.
+// M + X come back to M by 2^X, after the division so that this step overflows nothing
+// that the result does not.  A row that sees no key (l = 0): zeros and -inf.  No other row has l = 0: M is one of the
+// rounded scores, and lies at most kSlack below the largest, whose weight is therefore at least 1.
 template <int D>
-__device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, int c, float4 acc, float M, float MV, float L) {
+__device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, int c, float4 acc, float M, float X, float L) {
     const bool none = L == 0.f;
-    const float inv = none ? 0.f : 1.f / L, f = none ? 0.f : exp2f(MV - M);
+    const float inv = none ? 0.f : 1.f / L, f = none ? 0.f : exp2f(X);
     uint2 y;
     y.x = none ? 0u : bf16_pair(acc.x * inv * f, acc.y * inv * f);
     y.y = none ? 0u : bf16_pair(acc.z * inv * f, acc.w * inv * f);
@@ -147,27 +154,28 @@ __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, in
 constexpr int kBatch = 8;
 
 struct RowState {
-    float m = kNoMax, v = kNoMax, l = 0.f;       // references of the sum and of the weighted sum, sum
+    float m = kNoMax, x = 0.f, l = 0.f;       // reference of the sum; the weighted sum's, less that; sum
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 
-    __device__ __forceinline__ void move(float m1, float v1) {
-        const float f = ex2(v - v1);
+    // references m1 >= m and m1 + x1 >= m + x
+    __device__ __forceinline__ void move(float m1, float x1) {
+        const float f = ex2((m - m1) + x - x1);
         l *= ex2(m - m1);
         acc.x *= f;
         acc.y *= f;
         acc.z *= f;
         acc.w *= f;
         m = m1;
-        v = v1;
+        x = x1;
     }
-    // a state (m, v, l of q; x) whose references are not above this one's
-    __device__ __forceinline__ void add(float4 q, float4 x) {
-        const float f = ex2(q.y - v);
+    // a state (m, x, l of q; its weighted sum y) whose references are not above this one's
+    __device__ __forceinline__ void add(float4 q, float4 y) {
+        const float f = ex2((q.x - m) + q.y - x);
         l = fmaf(q.z, ex2(q.x - m), l);
-        acc.x = fmaf(x.x, f, acc.x);
-        acc.y = fmaf(x.y, f, acc.y);
-        acc.z = fmaf(x.z, f, acc.z);
-        acc.w = fmaf(x.w, f, acc.w);
+        acc.x = fmaf(y.x, f, acc.x);
+        acc.y = fmaf(y.y, f, acc.y);
+        acc.z = fmaf(y.z, f, acc.z);
+        acc.w = fmaf(y.w, f, acc.w);
     }
 };
 
@@ -190,7 +198,7 @@ __device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, 
                 const float* from = p.part + (size_t)(ck == c0 ? first_slot : 2 * ck) * PART + r * (D + 4);
 #pragma unroll
                 for (int i = 0; i < ROWS; ++i) {
-                    q[i][k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+                    q[i][k] = make_float4(kNoMax, 0.f, 0.f, 0.f);
                     x[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (ck <= c1 && r + i < rows) {
                         q[i][k] = __ldcg(reinterpret_cast<const float4*>(from + i * (D + 4) + D));
@@ -200,13 +208,13 @@ __device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, 
             }
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                float m1 = to[i].m, v1 = to[i].v;
+                float m1 = to[i].m;
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    m1 = fmaxf(m1, q[i][k].x);
-                    v1 = fmaxf(v1, q[i][k].y);
-                }
-                to[i].move(m1, v1);
+                for (int k = 0; k < kBatch; ++k) m1 = fmaxf(m1, q[i][k].x);
+                float x1 = (to[i].m - m1) + to[i].x;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) x1 = fmaxf(x1, (q[i][k].x - m1) + q[i][k].y);
+                to[i].move(m1, x1);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) to[i].add(q[i][k], x[i][k]);
             }
@@ -216,7 +224,7 @@ __device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, 
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 scratch[(warp * ROWS + i) * 33 + lane] = to[i].acc;
-                if (lane == 0) scratch[(warp * ROWS + i) * 33 + 32] = make_float4(to[i].m, to[i].v, to[i].l, 0.f);
+                if (lane == 0) scratch[(warp * ROWS + i) * 33 + 32] = make_float4(to[i].m, to[i].x, to[i].l, 0.f);
             }
             __syncthreads();
             if (part == 0)
@@ -224,14 +232,15 @@ __device__ __forceinline__ void attn_join(const PagedParams& p, int c0, int c1, 
 #pragma unroll
                     for (int i = 0; i < ROWS; ++i) {
                         const float4 q = scratch[(w * ROWS + i) * 33 + 32];
-                        to[i].move(fmaxf(to[i].m, q.x), fmaxf(to[i].v, q.y));
+                        const float m1 = fmaxf(to[i].m, q.x);
+                        to[i].move(m1, fmaxf((to[i].m - m1) + to[i].x, (q.x - m1) + q.y));
                         to[i].add(q, scratch[(w * ROWS + i) * 33 + lane]);
                     }
         }
         if (part == 0 && lane < D / 4)
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
-                if (r + i < rows) attn_finish<D>(p, row + r + i, lane, to[i].acc, to[i].m, to[i].v, to[i].l);
+                if (r + i < rows) attn_finish<D>(p, row + r + i, lane, to[i].acc, to[i].m, to[i].x, to[i].l);
     }
 }
 
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         float fac[NT][2];
         if (C::kSharedQ) {
             uint2 f[C::kSteps];
-            const float one = raw[0].fragments(p.sl2, f);
+            const float one = raw[0].fragments(f);
             if (warp < NT) {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s)
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float one = raw[C::kSharedQ ? 0 : nt].fragments(p.sl2, qf + (C::kSharedQ ? 0 : nt * C::kSteps));
+                const float one = raw[C::kSharedQ ? 0 : nt].fragments(qf + (C::kSharedQ ? 0 : nt * C::kSteps));
                 fac[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
                 fac[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }
@@ -343,9 +352,9 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         };
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        // m: reference of the sum, within kSlack of the scores' maximum; r: of the weights (bf16: m); l: sum
-        // mr: 2^(m - r)
-        float o[D / 16][NT][4], m[NT][2], r[NT][2], mr[NT][2], l[NT][2];
+        // m: reference of the sum, within kSlack of the scores' maximum; m + x: of the weights (bf16: x = 0);
+        // mx: 2^-x; l: sum
+        float o[D / 16][NT][4], m[NT][2], x[NT][2], mx[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -356,9 +365,9 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[nt][j] = r[nt][j] = kNoMax;
-                mr[nt][j] = 1.f;
-                l[nt][j] = 0.f;
+                m[nt][j] = kNoMax;
+                x[nt][j] = l[nt][j] = 0.f;
+                mx[nt][j] = 1.f;
             }
         bool tame = true;       // e4m3: every value scale so far within 2^-40 .. 2^40
 
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                 return key0 + x * kTileKeys + g + 8 * k < limit(nt, j) && !((bad >> ((i & 15) * 2 + x)) & 1u);
             };
 
-            // S^T, not yet scaled by fac
+            // S^T, scores in base 2 but for the row's power of two fac (e4m3)
             float s[H][NT][4];
             if (some) {
 #pragma unroll
@@ -421,18 +430,17 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         }
                     }
                 }
-                if (F8) {
 #pragma unroll
-                    for (int x = 0; x < H; ++x) {
-                        const float k0 = exp_scale(lds8(cur + C::kExps + x * 16 + g)), k1 = exp_scale(lds8(cur + C::kExps + x * 16 + 8 + g));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            s[x][nt][0] *= k0;
-                            s[x][nt][1] *= k0;
-                            s[x][nt][2] *= k1;
-                            s[x][nt][3] *= k1;
-                        }
+                for (int x = 0; x < H; ++x) {
+                    float k[2] = {p.sl2, p.sl2};
+                    if (F8) {
+                        k[0] *= exp_scale(lds8(cur + C::kExps + x * 16 + g));
+                        k[1] *= exp_scale(lds8(cur + C::kExps + x * 16 + 8 + g));
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[x][nt][c] = __fmul_rn(s[x][nt][c], k[c >> 1]);
                 }
                 if (edge) {
 #pragma unroll
@@ -469,10 +477,10 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     const uint32_t e = lds8(cur + C::kExps + x * 16 + 8 * k + g);
                     return edge && !(key0 + x * 16 + 8 * k + g < len && !((bad >> ((i & 15) * 2 + x)) & 1u)) ? 127u : e;
                 };
-                // The lane's own maxima of the scores, and of the scores times the values' scales, against
-                // the references: only where one lies beyond them do the 8 lanes with this t exchange
-                // maxima and the sums move.
-                float lm[NT][2], lr[NT][2];
+                // The lane's own maxima lm of the scores, and lm + hi of the scores times the values' scales (near:
+                // its bound), against the references: only where one lies beyond them do the 8 lanes with
+                // this t exchange maxima and the sums move.
+                float lm[NT][2], hi[NT][2];
                 bool grew = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -480,55 +488,56 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                     for (int j = 0; j < 2; ++j) {
                         float top = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
                         if (H == 2) top = fmaxf(top, fmaxf(s[H - 1][nt][j], s[H - 1][nt][j + 2]));
-                        lm[nt][j] = top * fac[nt][j];
-                        lr[nt][j] = lm[nt][j] + (float)e_max;
+                        lm[nt][j] = F8 ? top * fac[nt][j] : top;
+                        hi[nt][j] = (float)e_max;
                         grew |= lm[nt][j] > m[nt][j] + kSlack;
                     }
                 if (F8) {
                     if (!near) {
                         float ev[H][2];
 #pragma unroll
-                        for (int x = 0; x < H; ++x)
+                        for (int y = 0; y < H; ++y)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) ev[x][k] = (float)((int)value_exp(x, k) - 127);
+                            for (int k = 0; k < 2; ++k) ev[y][k] = (float)((int)value_exp(y, k) - 127);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                lr[nt][j] = kNoMax;
+                                hi[nt][j] = kNoMax;      // stays where the lane's keys are all masked (lm = -inf)
 #pragma unroll
-                                for (int x = 0; x < H; ++x)
+                                for (int y = 0; y < H; ++y)
 #pragma unroll
                                     for (int k = 0; k < 2; ++k)
-                                        lr[nt][j] = fmaxf(lr[nt][j], fmaf(s[x][nt][j + 2 * k], fac[nt][j], ev[x][k]));
+                                        hi[nt][j] = fmaxf(hi[nt][j], fmaf(s[y][nt][j + 2 * k], fac[nt][j], -lm[nt][j]) + ev[y][k]);
                             }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) grew |= lr[nt][j] > r[nt][j] + kSlack;
+                        for (int j = 0; j < 2; ++j) grew |= (lm[nt][j] - m[nt][j]) + hi[nt][j] > x[nt][j] + kSlack;
                 }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float top = lm[nt][j], ref = lr[nt][j];
+                            float top = lm[nt][j];
 #pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) {
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                                if (F8) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-                            }
+                            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                             top = fmaxf(m[nt][j], top);
-                            float a = ex2(m[nt][j] - top);
+                            const float by = m[nt][j] - top;
+                            float a = ex2(by);
                             l[nt][j] *= a;
-                            m[nt][j] = top;
                             if (F8) {
-                                ref = fmaxf(r[nt][j], ref);
-                                a = ex2(r[nt][j] - ref);
-                                r[nt][j] = ref;
-                                mr[nt][j] = ex2(top - ref);
+                                float ref = (lm[nt][j] - top) + hi[nt][j];
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+                                ref = fmaxf(by + x[nt][j], ref);
+                                a = ex2(by + x[nt][j] - ref);
+                                x[nt][j] = ref;
+                                mx[nt][j] = ex2(-ref);
                             }
+                            m[nt][j] = top;
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 o[k][nt][j] *= a;
@@ -540,14 +549,14 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                 uint32_t ph[H][NT][2], pl[H][NT][2];    // B fragments of P^T: hi and lo (bf16), or P' (fp16)
                 if (F8 && !near) {
 #pragma unroll
-                    for (int x = 0; x < H; ++x) {
-                        const float ev[2] = {(float)((int)value_exp(x, 0) - 127), (float)((int)value_exp(x, 1) - 127)};
+                    for (int y = 0; y < H; ++y) {
+                        const float ev[2] = {(float)((int)value_exp(y, 0) - 127), (float)((int)value_exp(y, 1) - 127)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                const float q = fmaf(s[x][nt][c], fac[nt][c & 1], -m[nt][c & 1]);
-                                s[x][nt][c] = ex2(fmaf(s[x][nt][c], fac[nt][c & 1], ev[c >> 1]) - r[nt][c & 1]);
+                                const float q = fmaf(s[y][nt][c], fac[nt][c & 1], -m[nt][c & 1]);
+                                s[y][nt][c] = ex2(q + (ev[c >> 1] - x[nt][c & 1]));
                                 l[nt][c & 1] += ex2(q);
                             }
                     }
@@ -558,29 +567,30 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         for (int j = 0; j < 2; ++j) {
                             float sum = 0.f;
 #pragma unroll
-                            for (int x = 0; x < H; ++x)
+                            for (int y = 0; y < H; ++y)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
-                                    const float q = ex2(fmaf(s[x][nt][j + 2 * k], fac[nt][j], -m[nt][j]));
+                                    const float z = s[y][nt][j + 2 * k];
+                                    const float q = ex2(F8 ? fmaf(z, fac[nt][j], -m[nt][j]) : __fsub_rn(z, m[nt][j]));
                                     sum += q;
-                                    s[x][nt][j + 2 * k] = q;
+                                    s[y][nt][j + 2 * k] = q;
                                 }
                             l[nt][j] += sum;
                         }
                     if (F8) {
                         float kv[H][2];
 #pragma unroll
-                        for (int x = 0; x < H; ++x)
+                        for (int y = 0; y < H; ++y)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) kv[x][k] = exp_scale(value_exp(x, k));
+                            for (int k = 0; k < 2; ++k) kv[y][k] = exp_scale(value_exp(y, k));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                                for (int x = 0; x < H; ++x)
+                                for (int y = 0; y < H; ++y)
 #pragma unroll
-                                    for (int k = 0; k < 2; ++k) s[x][nt][j + 2 * k] *= mr[nt][j] * kv[x][k];
+                                    for (int k = 0; k < 2; ++k) s[y][nt][j + 2 * k] *= mx[nt][j] * kv[y][k];
                             }
                     }
                 }
@@ -697,14 +707,14 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float x = l[nt][j];
+                float sum = l[nt][j];
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 if (g == 0) {
                     float* e = stats + warp * 3 * C::kRows + nt * 8 + 2 * t + j;
                     e[0] = m[nt][j];
-                    e[C::kRows] = F8 ? r[nt][j] : m[nt][j];
-                    e[2 * C::kRows] = x;
+                    e[C::kRows] = F8 ? x[nt][j] : 0.f;
+                    e[2 * C::kRows] = sum;
                 }
             }
         float* mine = reinterpret_cast<float*>(smem + warp * C::kWarp);
@@ -725,29 +735,29 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         const int rows = min(C::kRows, p.rows - row0);
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kPagedThreads) {
             const int i = idx / (D / 4), c = idx % (D / 4);
-            float M = kNoMax, MV = kNoMax, L = 0.f;
+            float M = kNoMax, X = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kPagedWarps; ++w) {
-                M = fmaxf(M, stats[(w * 3) * C::kRows + i]);
-                MV = fmaxf(MV, stats[(w * 3 + 1) * C::kRows + i]);
-            }
+            for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, stats[(w * 3) * C::kRows + i]);
+#pragma unroll
+            for (int w = 0; w < kPagedWarps; ++w)
+                X = fmaxf(X, (stats[(w * 3) * C::kRows + i] - M) + stats[(w * 3 + 1) * C::kRows + i]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kPagedWarps; ++w) {
-                const float f = ex2(stats[(w * 3) * C::kRows + i] - M), fv = ex2(stats[(w * 3 + 1) * C::kRows + i] - MV);
-                L = fmaf(stats[(w * 3 + 2) * C::kRows + i], f, L);
-                const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kWarp + (i * C::kStride + 4 * c) * 4);
-                acc.x = fmaf(x.x, fv, acc.x);
-                acc.y = fmaf(x.y, fv, acc.y);
-                acc.z = fmaf(x.z, fv, acc.z);
-                acc.w = fmaf(x.w, fv, acc.w);
+                const float by = stats[(w * 3) * C::kRows + i] - M, fv = ex2(by + stats[(w * 3 + 1) * C::kRows + i] - X);
+                L = fmaf(stats[(w * 3 + 2) * C::kRows + i], ex2(by), L);
+                const float4 y = *reinterpret_cast<const float4*>(smem + w * C::kWarp + (i * C::kStride + 4 * c) * 4);
+                acc.x = fmaf(y.x, fv, acc.x);
+                acc.y = fmaf(y.y, fv, acc.y);
+                acc.z = fmaf(y.z, fv, acc.z);
+                acc.w = fmaf(y.w, fv, acc.w);
             }
             if (whole) {
-                attn_finish<D>(p, qrow + row0 + i, c, acc, M, MV, L);
+                attn_finish<D>(p, qrow + row0 + i, c, acc, M, X, L);
             } else {
                 float* to = part + i * C::kStride;
                 *reinterpret_cast<float4*>(to + 4 * c) = acc;
-                if (c == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, MV, L, 0.f);
+                if (c == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, X, L, 0.f);
             }
         }
         if (!whole && p.arrived) {

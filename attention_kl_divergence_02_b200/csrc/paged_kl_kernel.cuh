@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         float fac1[NT][2], fac2[NT][2];       // of query 2t + j
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float f1 = raw1[nt].fragments(p.sl2, qf1 + nt * C::kSteps), f2 = raw2[nt].fragments(p.sl2, qf2 + nt * C::kSteps);
+            const float f1 = raw1[nt].fragments(qf1 + nt * C::kSteps), f2 = raw2[nt].fragments(qf2 + nt * C::kSteps);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 fac1[nt][j] = __shfl_sync(0xffffffffu, f1, 8 * t + 4 * j);
@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
             const int key0 = key00 + i * C::kUnit;
             if (key0 >= len) continue;
 
-            // scores in base 2, their difference, and whether a lane's references have to move
+            // scores in base 2, each rounded once (and never fused into a later difference), their difference, and
+            // whether a lane's references have to move
             float u[H][NT][2][2], v[H][NT][2][2], d[H][NT][2][2];
             bool grew = false;
 #pragma unroll
@@ -218,14 +219,14 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                     for (int c = 0; c < 4; ++c) s1[nt][c] = s2[nt][c] = 0.f;
                 tile_scores<D, F1, NT, SHARED>(ks + x * K1::kBytes, at1, qf1, s1, qf2, s2);
                 if (!SHARED) tile_scores<D, F2, NT, false>(ks + C::kOff2 + x * K2::kBytes, at2, qf2, s2, nullptr, nullptr);
-                float k1[2] = {1.f, 1.f}, k2[2] = {1.f, 1.f};
+                float k1[2] = {p.sl2, p.sl2}, k2[2] = {p.sl2, p.sl2};
                 if (F1) {
-                    k1[0] = exp_scale(lds8(ks + C::kExp1 + x * 16 + g));
-                    k1[1] = exp_scale(lds8(ks + C::kExp1 + x * 16 + 8 + g));
+                    k1[0] *= exp_scale(lds8(ks + C::kExp1 + x * 16 + g));
+                    k1[1] *= exp_scale(lds8(ks + C::kExp1 + x * 16 + 8 + g));
                 }
                 if (F2) {
-                    k2[0] = SHARED ? k1[0] : exp_scale(lds8(ks + C::kExp2 + x * 16 + g));
-                    k2[1] = SHARED ? k1[1] : exp_scale(lds8(ks + C::kExp2 + x * 16 + 8 + g));
+                    k2[0] = SHARED ? k1[0] : p.sl2 * exp_scale(lds8(ks + C::kExp2 + x * 16 + g));
+                    k2[1] = SHARED ? k1[1] : p.sl2 * exp_scale(lds8(ks + C::kExp2 + x * 16 + 8 + g));
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -233,9 +234,9 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            float y = s1[nt][j + 2 * k] * fac1[nt][j], z = s2[nt][j + 2 * k] * fac2[nt][j];
-                            if (F1) y *= k1[k];
-                            if (F2) z *= k2[k];
+                            float y = __fmul_rn(s1[nt][j + 2 * k], k1[k]), z = __fmul_rn(s2[nt][j + 2 * k], k2[k]);
+                            if (F1) y = __fmul_rn(y, fac1[nt][j]);
+                            if (F2) z = __fmul_rn(z, fac2[nt][j]);
                             u[x][nt][j][k] = y;
                             v[x][nt][j][k] = z;
                             d[x][nt][j][k] = y - z;
