@@ -54,6 +54,8 @@ struct PagedParams {
     int whole;             // segments are not cut: no partial states
     int grid;              // CTAs of the main kernel
     float sl2;             // scale * log2(e)
+    float mant;            // the same as mant * 2^exp, mant in [1, 2)
+    int exp;
     uint16_t* out;         // attention
     float* lse1;
     float* lse2;           // divergence
@@ -419,6 +421,33 @@ __device__ __forceinline__ int query_exponent(float top) {
 // 2^e for an exponent byte e + 127 of 1..254.
 __device__ __forceinline__ float exp_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 2^n for any n up to 127, by way of the subnormal numbers and never 0.
+__device__ __forceinline__ float pow2_down(int n) { return n >= -126 ? pow2(n) : __uint_as_float(1u << max(n + 149, 0)); }
+
+// How an e4m3 key's product with a stretched query row becomes a score in base 2: times
+// (mant * 2^c * the key's scale), which is rounded, times 2^(e + exp - c), the row's, which is exact.
+// c = -24 keeps the first factor in range for any row: a product is below 2^31, so with scales of
+// 2^-96 to 2^120 neither it nor its factor overflows or loses bits, and a score is right however large its
+// key and small its query are, or the other way round.  Only where a row of the block exceeds 2^118 or so, c
+// is higher, for the row's factor to exist.
+struct ScoreScale {
+    float key;       // to be multiplied by the key's scale
+    int shift;       // of a row's e
+
+    // e: exponents (Queries::fragments) of the lane's rows 2t + j of every block; all lanes call
+    template <int NT>
+    __device__ __forceinline__ void start(const PagedParams& p, const int (*e)[2]) {
+        int top = e[0][0];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) top = max(top, max(e[nt][0], e[nt][1]));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int c = max(-24, top + p.exp - 127);
+        key = p.mant * pow2(c);
+        shift = p.exp - c;
+    }
+    __device__ __forceinline__ float row(int e) const { return pow2_down(e + shift); }
+};
 
 __device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {   // 0 for infinities and NaN
     const uint32_t x = bf16_bits & 0x7fffu;
@@ -445,16 +474,16 @@ struct Queries {
             v[u] = have ? *reinterpret_cast<const uint4*>(src + col) : make_uint4(0, 0, 0, 0);
         }
     }
-    // frag[s] of every k-step; returns the power of two by which the products of row lane / 4 are to be
-    // multiplied (1 for bf16 keys), beside the scale and the key's own scale
-    __device__ __forceinline__ float fragments(uint2* frag) const {
+    // frag[s] of every k-step; returns the exponent e of the power of two by which the products of row lane / 4
+    // are to be multiplied (e4m3 keys)
+    __device__ __forceinline__ int fragments(uint2* frag) const {
         if (!F8) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 frag[2 * u] = make_uint2(v[u].x, v[u].y);
                 frag[2 * u + 1] = make_uint2(v[u].z, v[u].w);
             }
-            return 1.f;
+            return 0;
         }
         float top = 0.f;
 #pragma unroll
@@ -476,7 +505,7 @@ struct Queries {
             frag[2 * u] = make_uint2(h[0], h[1]);
             frag[2 * u + 1] = make_uint2(h[2], h[3]);
         }
-        return pow2(e);
+        return e;
     }
 };
 

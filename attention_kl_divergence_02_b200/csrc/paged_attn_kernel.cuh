@@ -8,7 +8,7 @@
 // a fused s * factor - m of any factor, the largest key's would be its product's rounding error, 2^(E - 24) for
 // a score near 2^E, and from 2^30 on weights would all vanish or overflow.  So a bf16 cache's products are
 // multiplied by the scale first; an e4m3 cache's by scale times key scale, and what is left, the query row's
-// power of two, may be fused, because that product is exact.
+// power of two, may be fused, because that product is exact (see ScoreScale).
 //
 // Bound: every cached byte is read once and used for 2 flops per query row and element, so with the
 // few rows of a KV head (Hq / Hkv * NQ) the floor is cache bytes / HBM bandwidth.  Everything here
@@ -322,29 +322,38 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 
         // queries of this segment, as B fragments
         uint2 qf[C::kSharedQ ? 1 : NT * C::kSteps];
-        float fac[NT][2];
+        int qe[NT][2];
         if (C::kSharedQ) {
             uint2 f[C::kSteps];
-            const float one = raw[0].fragments(f);
+            const int one = raw[0].fragments(f);
             if (warp < NT) {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s)
                     reinterpret_cast<uint2*>(smem + C::kQ)[(warp * C::kSteps + s) * 32 + lane] = f[s];
-                if (t == 0) reinterpret_cast<float*>(smem + C::kFactor)[warp * 8 + g] = one;
+                if (t == 0) reinterpret_cast<int*>(smem + C::kFactor)[warp * 8 + g] = one;
             }
             __syncthreads();
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                fac[nt][0] = reinterpret_cast<float*>(smem + C::kFactor)[nt * 8 + 2 * t];
-                fac[nt][1] = reinterpret_cast<float*>(smem + C::kFactor)[nt * 8 + 2 * t + 1];
+                qe[nt][0] = reinterpret_cast<int*>(smem + C::kFactor)[nt * 8 + 2 * t];
+                qe[nt][1] = reinterpret_cast<int*>(smem + C::kFactor)[nt * 8 + 2 * t + 1];
             }
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float one = raw[C::kSharedQ ? 0 : nt].fragments(qf + (C::kSharedQ ? 0 : nt * C::kSteps));
-                fac[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
-                fac[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
+                const int one = raw[C::kSharedQ ? 0 : nt].fragments(qf + (C::kSharedQ ? 0 : nt * C::kSteps));
+                qe[nt][0] = __shfl_sync(0xffffffffu, one, 8 * t);
+                qe[nt][1] = __shfl_sync(0xffffffffu, one, 8 * t + 4);
             }
+        }
+        ScoreScale scale;
+        float fac[NT][2];
+        if (F8) {
+            scale.start<NT>(p, qe);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fac[nt][j] = scale.row(qe[nt][j]);
         }
         // first key that a row does not see (of query 2t + j of block nt); the least over all rows
         auto limit = [&](int nt, int j) {
@@ -434,8 +443,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                 for (int x = 0; x < H; ++x) {
                     float k[2] = {p.sl2, p.sl2};
                     if (F8) {
-                        k[0] *= exp_scale(lds8(cur + C::kExps + x * 16 + g));
-                        k[1] *= exp_scale(lds8(cur + C::kExps + x * 16 + 8 + g));
+                        k[0] = scale.key * exp_scale(lds8(cur + C::kExps + x * 16 + g));
+                        k[1] = scale.key * exp_scale(lds8(cur + C::kExps + x * 16 + 8 + g));
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)

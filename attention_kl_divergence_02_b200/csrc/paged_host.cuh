@@ -171,6 +171,9 @@ int paged_params(const streamkl_cache* c, const int* table, int width, const int
     p->page_shift = page_shift_of(c->page_size);
     p->causal = causal ? 1 : 0;
     p->sl2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(p->sl2)) return STREAMKL_ERR_UNSUPPORTED;
+    p->mant = 2.f * std::frexp(p->sl2, &p->exp);
+    p->exp -= 1;
     p->arrived = static_cast<unsigned*>(workspace);
     p->part = reinterpret_cast<float*>(static_cast<char*>(workspace) + STREAMKL_PAGED_COUNTER_BYTES);
     return STREAMKL_OK;

@@ -172,16 +172,27 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
         for (int i = 0; i < C::kStages - 1; ++i) request(i, ring + i * C::kStage);
 
         uint2 qf1[NT * C::kSteps], qf2[NT * C::kSteps];
-        float fac1[NT][2], fac2[NT][2];       // of query 2t + j
+        int e1[NT][2], e2[NT][2];             // of query 2t + j
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float f1 = raw1[nt].fragments(qf1 + nt * C::kSteps), f2 = raw2[nt].fragments(qf2 + nt * C::kSteps);
+            const int f1 = raw1[nt].fragments(qf1 + nt * C::kSteps), f2 = raw2[nt].fragments(qf2 + nt * C::kSteps);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                fac1[nt][j] = __shfl_sync(0xffffffffu, f1, 8 * t + 4 * j);
-                fac2[nt][j] = __shfl_sync(0xffffffffu, f2, 8 * t + 4 * j);
+                e1[nt][j] = __shfl_sync(0xffffffffu, f1, 8 * t + 4 * j);
+                e2[nt][j] = __shfl_sync(0xffffffffu, f2, 8 * t + 4 * j);
             }
         }
+        ScoreScale scale1, scale2;
+        float fac1[NT][2], fac2[NT][2];
+        if (F1) scale1.start<NT>(p, e1);
+        if (F2) scale2.start<NT>(p, e2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (F1) fac1[nt][j] = scale1.row(e1[nt][j]);
+                if (F2) fac2[nt][j] = scale2.row(e2[nt][j]);
+            }
         // first key that a row does not see (of query 2t + j of block nt); the least over all rows
         auto limit = [&](int nt, int j) {
             return p.causal ? len - (p.NQ - 1) + (row0 + nt * 8 + 2 * t + j) % p.NQ : len;
@@ -220,13 +231,11 @@ __global__ void __launch_bounds__(kPagedThreads, KlCfg<D, F1, F2, SHARED, NT>::k
                 tile_scores<D, F1, NT, SHARED>(ks + x * K1::kBytes, at1, qf1, s1, qf2, s2);
                 if (!SHARED) tile_scores<D, F2, NT, false>(ks + C::kOff2 + x * K2::kBytes, at2, qf2, s2, nullptr, nullptr);
                 float k1[2] = {p.sl2, p.sl2}, k2[2] = {p.sl2, p.sl2};
-                if (F1) {
-                    k1[0] *= exp_scale(lds8(ks + C::kExp1 + x * 16 + g));
-                    k1[1] *= exp_scale(lds8(ks + C::kExp1 + x * 16 + 8 + g));
-                }
-                if (F2) {
-                    k2[0] = SHARED ? k1[0] : p.sl2 * exp_scale(lds8(ks + C::kExp2 + x * 16 + g));
-                    k2[1] = SHARED ? k1[1] : p.sl2 * exp_scale(lds8(ks + C::kExp2 + x * 16 + 8 + g));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float of1 = F1 ? exp_scale(lds8(ks + C::kExp1 + x * 16 + 8 * k + g)) : 1.f;
+                    if (F1) k1[k] = scale1.key * of1;
+                    if (F2) k2[k] = scale2.key * (SHARED ? of1 : exp_scale(lds8(ks + C::kExp2 + x * 16 + 8 * k + g)));
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
