@@ -31,9 +31,11 @@
 // instead of the sum m + x, in which scores beyond 2^24 would leave no bits for it.
 // Where a turn's scales lie within 2^kNear of each other (and all so far within 2^-40 .. 2^40), P' is
 // the sum's weight times two factors and m + x moves by the bound max s + max e, which is at most kNear too
-// high; elsewhere both are taken key by key, with a second exponential.  Too high a reference costs the
-// smallest weights bits below fp16's 2^-24: 2^-25 of the largest weight without, 2^-21 at worst with
-// the bound.
+// high; elsewhere both are taken key by key, with a second exponential.
+// fp16 ends at 2^-24, and weights that vanish there still count in l: many of them would pull the output
+// towards 0 (2^20 keys 25 octaves below a sink: 7.6 %, with the reference at the maximum).  So m + x moves
+// kDrop below the maximum, which with the slack uses fp16 up to 2^15: what is lost of a weight is at most 2^-32
+// of the warp's largest P', 2^-28 with the bound.
 #pragma once
 
 #include "paged.cuh"
@@ -41,6 +43,7 @@
 namespace skl {
 
 constexpr int kNear = 4;      // octaves, see above
+constexpr float kDrop = 7.f;  // the same; 2^(kDrop + kSlack) is below fp16's largest, 65504
 
 // Values: lane (g, t) of V^T's fragments holds columns of keys 2t, 2t + 1, 2t + 8 and 2t + 9, and takes
 // kElems contiguous ones of each: chunk g (and g + 8 where a row has 16), or half a chunk where it has
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         };
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        // m: reference of the sum, within kSlack of the scores' maximum; m + x: of the weights (bf16: x = 0);
-        // mx: 2^-x; l: sum
+        // m: reference of the sum, within kSlack of the scores' maximum; m + x: of the weights (bf16: x = 0), kDrop below
+        // what it follows; mx: 2^-x; l: sum
         float o[D / 16][NT][4], m[NT][2], x[NT][2], mx[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) grew |= (lm[nt][j] - m[nt][j]) + hi[nt][j] > x[nt][j] + kSlack;
+                        for (int j = 0; j < 2; ++j) grew |= (lm[nt][j] - m[nt][j]) + hi[nt][j] > x[nt][j] + (kSlack + kDrop);
                 }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                                 float ref = (lm[nt][j] - top) + hi[nt][j];
 #pragma unroll
                                 for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-                                ref = fmaxf(by + x[nt][j], ref);
+                                ref = fmaxf(by + x[nt][j], ref - kDrop);
                                 a = ex2(by + x[nt][j] - ref);
                                 x[nt][j] = ref;
                                 mx[nt][j] = ex2(-ref);

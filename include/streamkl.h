@@ -290,6 +290,9 @@ size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
  * A row that sees no key gets zeros and lse = -inf.  What lies in the cache behind a sequence's
  * length, or behind the last key that a row sees, does not reach the row's result even when it is
  * not finite.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
+ * Scores, sums and states are fp32.  Weights meet bf16 values as two bf16 terms (2^-16 of a weight); e4m3
+ * values as one fp16 term with the value's scale in it: 11 bits of each, and at least what
+ * exceeds 2^-28 of the largest such product of a row.
  *   workspace : at least streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d) bytes, its counters zero (see
  *               there).  Two calls that can run at the same time need two workspaces.
  * One or two kernels; the result does not depend on the order in which CTAs run.

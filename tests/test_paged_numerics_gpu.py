@@ -1,5 +1,5 @@
-"""Paged attention and divergence of scores far beyond the usual, and of keys and queries of extreme and
-opposite size."""
+"""Paged attention and divergence where an error would not show among random keys: many small weights beside a
+large one, scores far beyond the usual, keys and queries of extreme and opposite size."""
 import math
 
 import pytest
@@ -10,6 +10,50 @@ from attention_kl_divergence_02_b200 import binding
 import paged_ref as ref
 
 pytestmark = pytest.mark.gpu
+
+
+def shared_rows(case, B):
+    """Table and lengths of B sequences that all are the case's only one."""
+    return case.table.expand(B, -1).contiguous(), case.len.expand(B).contiguous()
+
+
+# ------------------------------------------------------------------ one strong key, many weak ones
+@pytest.mark.parametrize("d,Hq,n,B", [(64, 1, 1 << 20, 448), (128, 20, 1 << 18, 300)])
+def test_many_weak_keys_beside_a_strong_one(d, Hq, n, B):
+    """One key outweighs each of the others by 2^25.2, their values are 16 times its own, and enough
+    sequences share the pages that a CTA folds a whole one: what one warp leaves out of the weighted
+    sum, but not of the sum of weights, shows as a bias."""
+    c = ref.Case([n], 1, d, 1024, "e4m3", seed=1)
+    c.k[0].zero_()
+    # 25.157 octaves = 17.4375 in natural units, of which every column gives 1 / d; 2.25 is an e4m3 number
+    c.k[0][:, 5] = 2.25
+    scale = 0.125 * 64 / d
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    v = torch.randint(8, 16, (1, n, d), generator=g, device="cuda").float()      # 4 bits: exact
+    v[:, 5] /= 16
+    c.v[0] = v.to(torch.bfloat16)
+    c.fill()
+    q = torch.full((B, Hq, 1, d), 0.96875, dtype=torch.bfloat16, device="cuda")
+    table, lengths = shared_rows(c, B)
+    out, lse = binding.paged_attn(q, c.cache, table, lengths, scale=scale)
+    s = torch.zeros(n, dtype=torch.float64, device="cuda")
+    s[5] = 0.96875 * 2.25 * d * scale
+    p = torch.softmax(s, 0)
+    want = p @ c.vc[0][0]
+    # the output's rounding; one fp16 rounding of each weight (2^-11) and what exp2 and the rescalings leave;
+    # a warp's fp32 sums: at most every fourth tile of 16 keys is its own
+    tol = want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20 + (n / 64) * 2.0 ** -23)
+    # weights below fp16's normal numbers: half its smallest step, 2^-25, of a reference that lies at most
+    # 2^4 (a bound) / 2^7 above the largest p_j 2^e_j, for each of a warp's n / 4 codes of at most 448
+    row = c.vc[0][0].abs().amax(-1)
+    unit = torch.exp2(torch.ceil(torch.log2(row / 448)))
+    tol = tol + n / 4 * 2.0 ** -28 * 448 * float((p * unit).max())
+    assert float((tol / want).max()) < 0.012         # the test means something: a quarter of the weak keys are 2.3 to 7.6 %
+    ref.close(out, want.expand_as(out), tol.expand_as(out), "out")
+    want_lse = torch.logsumexp(s, 0).expand_as(lse)
+    # scores are exact products of a few bits each but for the scale's factor log2(e)
+    ref.close(lse, want_lse, want_lse * 2.0 ** -21 + 2.0 ** -21 + (n / 64) * 2.0 ** -23, "lse")
 
 
 # ------------------------------------------------------------------ large scores
