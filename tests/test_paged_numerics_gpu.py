@@ -1,5 +1,6 @@
-"""Paged attention and divergence where an error would not show among random keys: many small weights beside a
-large one, scores far beyond the usual, keys and queries of extreme and opposite size."""
+"""Paged attention and divergence where a small error would not show among random keys: many small weights
+beside a large one, scores far beyond the usual, keys and queries of extreme and opposite size, and every value
+tile of a long sequence accounted for."""
 import math
 
 import pytest
@@ -166,3 +167,77 @@ def test_divergence_of_keys_and_queries_of_opposite_size(kinds, keys, gain, by):
     ref.close(got[0], kl, tol, "kl")
     ref.close(got[1], lse1, tol_lse, "lse1")
     ref.close(got[2], lse2, tol_lse, "lse2")
+
+
+# ------------------------------------------------------------------ every tile of a long sequence
+LONG = [
+    # Hq, Hkv, NQ, d, page, kind, causal, lengths
+    (16, 16, 1, 64, 1024, "e4m3", True, [65600]),
+    (16, 16, 1, 128, 1024, "bf16", True, [62001]),
+    (4, 1, 5, 128, 16, "e4m3", True, [20011, 3000, 0, 17, 9999]),      # 20 rows
+    (4, 1, 8, 128, 32, "bf16", True, [30003, 511]),                    # 32 rows
+    (8, 2, 3, 64, 16, "bf16", True, [33333, 64, 2049]),                # 12 rows
+    (7, 1, 1, 128, 64, "e4m3", True, [131072 - 15]),
+    (2, 1, 1, 64, 16, "e4m3", True, [900] * 150),                      # dealt out whole
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "q%dkv%dn%dd%dp%d%sB%d" % (*c[:6], len(c[7])))
+def test_every_value_counts_once(case):
+    """Keys of zeros weigh every value alike, and the values are small whole numbers: all sums are exact, so a
+    tile that is lost, doubled, or taken from another place changes the mean beyond its rounding."""
+    Hq, Hkv, NQ, d, page, kind, causal, lengths = case
+    c = ref.Case(lengths, Hkv, d, page, kind, seed=40)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(41)
+    for b, n in enumerate(lengths):
+        c.k[b].zero_()
+        c.v[b] = torch.randint(-16, 17, (Hkv, n, d), generator=g, device="cuda").to(torch.bfloat16)
+    c.fill()
+    q = ref.queries(len(lengths), Hq, NQ, d, seed=42)
+    out, lse = binding.paged_attn(q, c.cache, c.table, c.len, causal=causal)
+    for b, n in enumerate(lengths):
+        upto = torch.cat([torch.zeros((Hkv, 1, d), dtype=torch.float64, device="cuda"), c.vc[b].cumsum(1)], 1)
+        for i in range(NQ):
+            m = max(0, n - (NQ - 1 - i))
+            want = upto[:, m].repeat_interleave(Hq // Hkv, 0) / max(1, m)
+            # one rounding to bf16, half a step; 1 / l and two products in fp32
+            ref.close(out[b, :, i], want, want.abs() * (2.0 ** -8 + 2.0 ** -22), "sequence %d, token %d" % (b, i))
+            if m:
+                assert float((lse[b, :, i].double() - math.log(m)).abs().max()) <= 2.0 ** -21 + math.log(m) * 2.0 ** -22
+            else:
+                assert bool((lse[b, :, i] == -math.inf).all())
+
+
+@pytest.mark.parametrize("kind,d,n", [("e4m3", 64, 65600), ("bf16", 128, 62001), ("bf16", 64, 65551), ("e4m3", 128, 40000)])
+def test_a_key_meets_its_own_values(kind, d, n):
+    """Single keys at the borders of tiles, units, pages and batches of page entries (and elsewhere) win a row each:
+    the row is that key's values."""
+    Hkv, R = 16, 8
+    c = ref.Case([n], Hkv, d, 1024, kind, seed=50)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    border = [0, 15, 16, 31, 32, 47, 48, 63, 64, 127, 128, 511, 512, 1007, 1008, 1023, 1024, 1025, 2031, 2032, 2047, 2048,
+              2049, 4095, 4096, 8191, 8192, 16383, 16384, 32767, 32768, n - 17, n - 16, n - 2, n - 1]
+    other = torch.randperm(n, generator=g, device="cuda").tolist()
+    at = (border + [x for x in other if x not in border])[:Hkv * R]
+    u = torch.where(torch.rand((Hkv, R, d), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    at = torch.tensor(at, device="cuda").view(R, Hkv).t()                  # [Hkv, R]
+    k = 0.1 * torch.randn((Hkv, n, d), generator=g, device="cuda")
+    for h in range(Hkv):
+        k[h, at[h]] = u[h] * 512 / d                                       # score 512 / sqrt(d) of its own row
+    c.k[0] = k.to(torch.bfloat16)
+    c.fill()
+    q = u.unsqueeze(0).to(torch.bfloat16)                                  # [1, Hkv, R, d]
+    scale = d ** -0.5
+    out, lse = binding.paged_attn(q, c.cache, c.table, c.len, scale=scale, causal=False)
+    for h in range(Hkv):
+        s = q[0, h].double() @ c.kc[0][h].t() * scale
+        own = s.gather(1, at[h][:, None])
+        p = torch.softmax(s, -1)
+        assert float(p.gather(1, at[h][:, None]).min()) > 1 - 2.0 ** -12
+        want = p @ c.vc[0][h]
+        # the output's and the weight's rounding; the others, together under 2^-12, half off at most
+        tol = want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) + (1 - p.gather(1, at[h][:, None])) * float(c.vc[0][h].abs().max())
+        ref.close(out[0, h], want, tol, "head %d" % h)
+        ref.close(lse[0, h], own[:, 0], own[:, 0].abs() * 2.0 ** -20 + 2.0 ** -12, "lse")
