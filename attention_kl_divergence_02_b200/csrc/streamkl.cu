@@ -188,6 +188,20 @@ int launch_bwd(int mode, const CUtensorMap& q1, const CUtensorMap& q2, const CUt
     return launch_convert<D>(p.dq_ws, p.dq, p.B * p.Hq, p.NQ, p.nqt, p.scale, st, "dq convert launch");
 }
 
+// Synchronises, reads and clears a device status word.
+int take_status(const int& word, void* stream) {
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+    int v = 0, zero = 0;
+    e = cudaMemcpyFromSymbol(&v, word, sizeof(int));
+    if (e != cudaSuccess) return cuda_fail(e, "read device status");
+    if (v != 0) {
+        e = cudaMemcpyToSymbol(word, &zero, sizeof(int));
+        if (e != cudaSuccess) return cuda_fail(e, "clear device status");
+    }
+    return v;
+}
+
 }  // namespace
 
 extern "C" {
@@ -209,23 +223,8 @@ const char* streamkl_status_string(int status) {
 const char* streamkl_last_cuda_error(void) { return t_last_cuda_error; }
 
 int streamkl_device_status(void* stream) {
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    int v = 0, zero = 0;
-    e = cudaMemcpyFromSymbol(&v, skl::g_status, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "read device status");
-    if (v != 0) {
-        e = cudaMemcpyToSymbol(skl::g_status, &zero, sizeof(int));
-        if (e != cudaSuccess) return cuda_fail(e, "clear device status");
-    }
-    int page = 0;
-    e = cudaMemcpyFromSymbol(&page, skl::g_page_status, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "read device status");
-    if (page != 0) {
-        e = cudaMemcpyToSymbol(skl::g_page_status, &zero, sizeof(int));
-        if (e != cudaSuccess) return cuda_fail(e, "clear device status");
-    }
-    return v != 0 ? v : page;
+    const int status = take_status(skl::g_status, stream);
+    return status != STREAMKL_OK ? status : take_status(skl::g_page_status, stream);
 }
 
 int streamkl_selftest_watchdog(int starve, long long* waited_ns, void* stream) {
@@ -237,7 +236,7 @@ int streamkl_selftest_watchdog(int starve, long long* waited_ns, void* stream) {
     skl::streamkl_watchdog_kernel<<<1, 64, 0, st>>>(starve);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "watchdog launch");
-    const int status = streamkl_device_status(stream);   // synchronises, reads, clears
+    const int status = take_status(skl::g_status, stream);   // of its own waits: a page error stays recorded
     if (status == STREAMKL_ERR_CUDA) return status;
     unsigned long long res[3];
     e = cudaMemcpyFromSymbol(res, skl::g_watchdog, sizeof(res));

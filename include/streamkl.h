@@ -375,7 +375,8 @@ const char* streamkl_status_string(int status);
  * device.  Returns STREAMKL_OK, STREAMKL_ERR_TIMEOUT (a kernel abandoned a pipeline wait
  * and left its outputs undefined), STREAMKL_ERR_PAGE (a paged call met a table entry, position or
  * length outside the cache) or STREAMKL_ERR_CUDA (the synchronisation itself failed;
- * cudaGetLastError text is available through streamkl_last_cuda_error).
+ * cudaGetLastError text is available through streamkl_last_cuda_error).  Where both are recorded, the
+ * timeout is returned first and the page error by the next call.
  */
 int streamkl_device_status(void* stream);
 
@@ -387,8 +388,8 @@ int streamkl_device_status(void* stream);
  *   starve != 0: nothing completes them.  The first wait gives up after the library's
  *     wait limit (2 s), records STREAMKL_ERR_TIMEOUT and raises the CTA's abort flag; the
  *     second wait sees the flag and gives up at once.  Returns STREAMKL_ERR_TIMEOUT.
- * Nothing faults or traps; the context stays usable.  The device status word is read and
- * cleared like streamkl_device_status does.  If waited_ns is not NULL it receives the
+ * Nothing faults or traps; the context stays usable.  A timeout in the device status word is read and
+ * cleared like streamkl_device_status does; a page error stays recorded.  If waited_ns is not NULL it receives the
  * nanoseconds each of the two waits took.  Returns STREAMKL_ERR_CUDA if a CUDA call
  * failed.  Blocks the calling host thread for up to about 2.5 s.
  */
