@@ -136,7 +136,9 @@ PyObject* kl(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (n != 10 || !g_kl || !c.take(a[1], a[4], a[0], a[5], a[6], a[7], a[8], a[9])) return go_on();
         const auto* cache2 = static_cast<const streamkl_cache*>(PyLong_AsVoidPtr(a[3]));
         const at::Tensor* q2 = plain(a[2], at::kBFloat16, c.device, 4);
-        if (!cache2 || !q2 || q2->sizes() != c.q->sizes()) return go_on();
+        if (!cache2 || !q2 || q2->sizes() != c.q->sizes() || cache2->pages != c.cache->pages || cache2->Hkv != c.cache->Hkv ||
+            cache2->page_size != c.cache->page_size || cache2->d != c.cache->d)
+            return go_on();
         at::Tensor out[3] = {c.rows(), c.rows(), c.rows()};
         int rc;
         Py_BEGIN_ALLOW_THREADS
