@@ -435,13 +435,29 @@ _torch = None
 _fast = None
 
 
+def _load_fastcall():
+    """The extension that was built for this torch version; None where there is none that loads."""
+    import importlib.util
+    from . import build
+    import torch
+    path = build.fastcall_path(torch.__version__)
+    if not os.path.exists(path):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location(__package__ + "._fastcall", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:
+        return None
+    return module
+
+
 def _start():
     global _torch, _fast
     import torch
     _torch = torch
-    try:
-        from . import _fastcall
-    except ImportError:
+    _fastcall = _load_fastcall()
+    if _fastcall is None:
         return
     lib = load()
     _fastcall.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -1,5 +1,5 @@
-"""Paged calls from Python: both ways of a call (the extension and the plain path) refuse alike, and the device
-status loses nothing."""
+"""Paged calls from Python: the extension is what runs, both ways of a call refuse alike, and the device status
+loses nothing."""
 import pytest
 import torch
 
@@ -18,6 +18,28 @@ def batch(kind="bf16"):
     c = ref.Case([40, 20], 2, 64, 16, kind, seed=120)
     q = ref.queries(2, 4, 1, 64, seed=121)
     return c, q, binding.paged_workspace(2, 4, 2, 1, 64)
+
+
+def test_everyday_calls_run_in_the_extension(monkeypatch):
+    """It is loaded, takes the everyday case of every call itself, and agrees with the plain path."""
+    c, q, ws = batch()
+    assert binding._fast is not None
+    scale = 0.125
+    done = binding._fast.attn(q, c.cache.address, c.cache.index, c.table, c.len, scale, True, ws)
+    assert done is not NotImplemented and done[0] == binding.OK
+    kl = binding._fast.kl(q, c.cache.address, q, c.cache.address, c.cache.index, c.table, c.len, scale, True, ws)
+    assert kl is not NotImplemented and kl[0] == binding.OK
+    new = torch.zeros((2, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    zero, one = (torch.full((2,), x, dtype=torch.int32, device="cuda") for x in (0, 1))
+    assert binding._fast.move(c.cache.address, c.cache.index, False, new, new.clone(), c.table, None, one) == binding.OK
+    want = binding.paged_attn(q, c.cache, c.table, c.len, workspace=ws)
+    monkeypatch.setattr(binding, "_fast", None)
+    plain = binding.paged_attn(q, c.cache, c.table, c.len, workspace=ws)
+    for a, b in zip((*done[1:], *want), (*plain, *plain)):
+        assert torch.equal(a, b)
+    for a, b in zip(kl[1], binding.paged_kl(q, c.cache, q, c.cache, c.table, c.len, workspace=ws)):
+        assert torch.equal(a, b)
+    assert status() == binding.OK
 
 
 @pytest.mark.parametrize("fast", [True, False])
