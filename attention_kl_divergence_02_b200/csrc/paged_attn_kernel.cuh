@@ -24,7 +24,8 @@
 //
 // bf16 cache: P is split into two bf16 terms (hi + lo, off by 2^-16 of a weight), because one bf16 rounding
 // of P (2^-8) would add as much error as the output's own rounding; the tensor pipe has room for the
-// second product.
+// second product.  hi is the largest bf16 number below P, so that lo is above 0 wherever P is: times an infinite
+// value both are that infinity (a lo of either sign, or 0, would make NaN of it).  What needs 8 bits is kept exactly.
 // e4m3 cache: values are met as fp16 (exact) without their scales 2^e_j; those go into the weights,
 // P'_j = 2^(s_j - m + e_j - x), where m + x follows the running maximum of s_j + e_j, so that P' stays within
 // fp16 whatever the scales are; its rounding (2^-11) is an eighth of the output's.  l keeps to m alone.  x is kept
@@ -41,6 +42,13 @@
 #include "paged.cuh"
 
 namespace skl {
+
+// The terms of two weights of 0 or more, as bf16 pairs (hi of 0 is 0).
+__device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& hi, uint32_t& lo) {
+    const int x0 = max(__float_as_int(w0) - 1, 0), x1 = max(__float_as_int(w1) - 1, 0);
+    hi = __byte_perm(x0, x1, 0x7632);
+    lo = bf16_pair(w0 - __uint_as_float(x0 & 0xffff0000u), w1 - __uint_as_float(x1 & 0xffff0000u));
+}
 
 constexpr int kNear = 4;      // octaves, see above
 constexpr float kDrop = 7.f;  // the same; 2^(kDrop + kSlack) is below fp16's largest, 65504
@@ -615,11 +623,13 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                             ph[x][nt][0] = movmatrix(pack_half(w[0], w[1]));
                             ph[x][nt][1] = movmatrix(pack_half(w[2], w[3]));
                         } else {
-                            const uint32_t h0 = bf16_pair(w[0], w[1]), h1 = bf16_pair(w[2], w[3]);
-                            ph[x][nt][0] = movmatrix(h0);
-                            ph[x][nt][1] = movmatrix(h1);
-                            pl[x][nt][0] = movmatrix(bf16_pair(w[0] - bf16_lo(h0), w[1] - bf16_hi(h0)));
-                            pl[x][nt][1] = movmatrix(bf16_pair(w[2] - bf16_lo(h1), w[3] - bf16_hi(h1)));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t hi, lo;
+                                weight_terms(w[2 * k], w[2 * k + 1], hi, lo);
+                                ph[x][nt][k] = movmatrix(hi);
+                                pl[x][nt][k] = movmatrix(lo);
+                            }
                         }
                     }
                 // O^T += V^T P^T
