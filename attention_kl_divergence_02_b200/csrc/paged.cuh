@@ -30,9 +30,10 @@ constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kTileKeys = 16;          // keys of a product (its M)
 constexpr float kNoMax = -3.402823466e38f;   // running maximum before any key
 // Running sums refer to 2^m with m within kSlack (log2 units) of the running maximum, and are rescaled only
-// when it grows beyond that: weights reach 2^8, which costs fp32 sums and the weights' 16-bit types
-// (relative rounding, fp16 up to 2^15) nothing, and the rescaling, in almost every turn of a short
-// sequence with many rows otherwise, all but vanishes.
+// when it grows beyond that, which costs fp32 sums and the weights' 16-bit types (relative rounding, fp16 up to
+// 2^15) nothing: the rescaling, in almost every turn of a short sequence with many rows otherwise, all but
+// vanishes.  Attention moves m to kSlack above the maximum, so that no weight exceeds 1 and the sums of weights
+// times values overflow no sooner than they must; the divergence, without values, moves it to the maximum.
 constexpr float kSlack = 8.f;
 
 struct PagedPool {

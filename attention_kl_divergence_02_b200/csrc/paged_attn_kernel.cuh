@@ -144,8 +144,8 @@ struct AttnCfg {
 
 // Four columns of a finished row: o / l, rounded once to bf16, and the row's lse.  Weights that refer to
 // M + X come back to M by 2^X, after the division so that this step overflows nothing
-// that the result does not.  A row that sees no key (l = 0): zeros and -inf.  No other row has l = 0: M is one of the
-// rounded scores, and lies at most kSlack below the largest, whose weight is therefore at least 1.
+// that the result does not.  A row that sees no key (l = 0): zeros and -inf.  No other row has l = 0: M is kSlack
+// above one of the rounded scores (rounded itself, by at most as much again), whose weight is therefore 2^-16 or more.
 template <int D>
 __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, int c, float4 acc, float M, float X, float L) {
     const bool none = L == 0.f;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
         };
         const int least = p.causal ? len - (p.NQ - 1) : len;
 
-        // m: reference of the sum, within kSlack of the scores' maximum; m + x: of the weights (bf16: x = 0), kDrop below
+        // m: reference of the sum, up to kSlack above the scores' maximum; m + x: of the weights (bf16: x = 0), kDrop below
         // what it follows; mx: 2^-x; l: sum
         float o[D / 16][NT][4], m[NT][2], x[NT][2], mx[NT][2], l[NT][2];
 #pragma unroll
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                         if (H == 2) top = fmaxf(top, fmaxf(s[H - 1][nt][j], s[H - 1][nt][j + 2]));
                         lm[nt][j] = F8 ? top * fac[nt][j] : top;
                         hi[nt][j] = (float)e_max;
-                        grew |= lm[nt][j] > m[nt][j] + kSlack;
+                        grew |= lm[nt][j] > m[nt][j];
                     }
                 if (F8) {
                     if (!near) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kPagedThreads, AttnCfg<D, F8, NT>::kCtas) stre
                             float top = lm[nt][j];
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                            top = fmaxf(m[nt][j], top);
+                            top = fmaxf(m[nt][j], top + kSlack);
                             const float by = m[nt][j] - top;
                             float a = ex2(by);
                             l[nt][j] *= a;

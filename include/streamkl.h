@@ -289,10 +289,10 @@ size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
  *             j <= length - NQ + i; zero: every token sees all keys.
  * A row that sees no key, or only scores of -inf, gets zeros and lse = -inf.  What lies in the cache
  * behind a sequence's length, or behind the last key that a row sees, does not reach the row's
- * result even when it is not finite.  An infinite value that a row sees with a weight of 2^-126 of the largest or
+ * result even when it is not finite.  An infinite value that a row sees with a weight of 2^-110 of the largest or
  * more makes its column that infinity (NaN with a smaller weight, with both infinities, or with NaN).
- * The sum of weights times values is divided at the end, and weights reach 2^8: it overflows, like any fp32 sum,
- * where bf16 values lie beyond 2^119 / (keys of such size).  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
+ * Sums of weights of at most 1 times values are divided at the end: they overflow, like any fp32 sum, where
+ * so many bf16 values are so large.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
  * Scores, sums and states are fp32.  Weights meet bf16 values as two bf16 terms (2^-16 of a weight); e4m3
  * values as one fp16 term with the value's scale in it: 11 bits of each, and at least what
  * exceeds 2^-28 of the largest such product of a row.
