@@ -289,13 +289,14 @@ size_t streamkl_paged_workspace_bytes(int B, int Hq, int Hkv, int NQ, int d);
  *             j <= length - NQ + i; zero: every token sees all keys.
  * A row that sees no key, or only scores of -inf, gets zeros and lse = -inf.  What lies in the cache
  * behind a sequence's length, or behind the last key that a row sees, does not reach the row's
- * result even when it is not finite.  An infinite value that a row sees with a weight of 2^-110 of the largest or
- * more makes its column that infinity (NaN with a smaller weight, with both infinities, or with NaN).
- * Sums of weights of at most 1 times values are divided at the end: they overflow, like any fp32 sum, where
- * so many bf16 values are so large.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of Hq / Hkv * NQ.
- * Scores, sums and states are fp32.  Weights meet bf16 values as two bf16 terms (2^-16 of a weight); e4m3
- * values as one fp16 term with the value's scale in it: 11 bits of each, and at least what
- * exceeds 2^-28 of the largest such product of a row.
+ * result even when it is not finite.  Any Hq / Hkv and NQ; the cache is read once per 32 rows of
+ * Hq / Hkv * NQ.
+ * Precision: scores, sums and states are fp32.  Weights are at most 1; over bf16 they count down to 2^-110 of a
+ * row's largest and meet the values as two bf16 terms (2^-16 of a weight); over e4m3 they meet them as one
+ * fp16 term with the value's scale in it, which keeps 11 bits, and at least what exceeds 2^-28 of the
+ * row's largest such product.  Sums of weights times values are divided at the end, and overflow like any
+ * fp32 sum where enough bf16 values are large enough.  An infinite value makes the columns of the rows that see it
+ * that infinity; NaN with both infinities, with NaN, or where the weight does not count.
  *   workspace : at least streamkl_paged_workspace_bytes(B, Hq, Hkv, NQ, d) bytes, its counters zero (see
  *               there).  Two calls that can run at the same time need two workspaces.
  * One or two kernels; the result does not depend on the order in which CTAs run.

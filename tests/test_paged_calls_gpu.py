@@ -73,3 +73,42 @@ def test_a_bad_page_does_not_reach_the_watchdog_s_self_test():
     rc, _ = binding.streamkl_selftest_watchdog(1)       # waits that run out, and return
     assert rc == binding.ERR_TIMEOUT
     assert status() == binding.ERR_PAGE and status() == binding.OK
+
+
+def test_a_captured_fork_and_join():
+    """Captured behind a copy, beside a call on another stream, and behind both: every launch is a programmatic
+    dependent of all that it has to wait for."""
+    c, q, _ = batch()
+    other = (q.float() * 2).to(torch.bfloat16)
+    want = [binding.paged_attn(x, c.cache, c.table, c.len) for x in (q, other)]
+    spaces = [binding.paged_workspace(2, 4, 2, 1, 64) for _ in range(2)]
+    out = [(torch.empty_like(q), torch.empty((2, 4, 1), device="cuda")) for _ in range(2)]
+    source, rows = q.clone(), torch.empty_like(q)
+    side = torch.cuda.Stream()
+
+    def step():
+        rows.copy_(source)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            binding.paged_attn(rows, c.cache, c.table, c.len, out=out[1], workspace=spaces[1])
+        binding.paged_attn(rows, c.cache, c.table, c.len, out=out[0], workspace=spaces[0])
+        torch.cuda.current_stream().wait_stream(side)
+        return binding.paged_attn(rows, c.cache, c.table, c.len)
+
+    first = torch.cuda.Stream()
+    first.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(first):
+        step()
+    torch.cuda.current_stream().wait_stream(first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.append(step())
+    for x, w in ((q, want[0]), (other, want[1]), (q, want[0])):
+        source.copy_(x)
+        for o in out:
+            o[0].zero_(), o[1].zero_()
+        graph.replay()
+        for o in out:
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    assert status() == binding.OK
