@@ -18,7 +18,7 @@
 // Per tile a warp computes S^T = K Q^T (16 keys x 8 rows per product) and the weights, and turns P^T around
 // with movmatrix into the B operand of O^T = V^T P^T (M: 16 columns of d, N: 8 rows, K: 16 keys).  V^T's
 // fragments need two keys' values of one column in a register: the lane loads the same bytes of four
-// keys and joins them with byte permutes.  The m16n8k16 products suffice: the tensor pipe is 11 to 18 %
+// keys and joins them with byte permutes.  The m16n8k16 products suffice: the tensor pipe is 14 to 19 %
 // busy, and without any one of the three steps the kernel takes as long (64 uneven sequences: 106 us
 // against 106 when that was measured); without the copies it takes 78.
 //
@@ -34,7 +34,7 @@
 // the sum's weight times two factors and m + x moves by the bound max s + max e, which is at most kNear too
 // high; elsewhere both are taken key by key, with a second exponential.
 // fp16 ends at 2^-24, and weights that vanish there still count in l: many of them would pull the output
-// towards 0 (2^20 keys 25 octaves below a sink: 7.6 %, with the reference at the maximum).  So m + x moves
+// towards 0 (2^20 keys 25 octaves below a sink: up to 9.7 % with the reference at the maximum).  So m + x moves
 // kDrop below the maximum, which with the slack uses fp16 up to 2^15: what is lost of a weight is at most 2^-32
 // of the warp's largest P', 2^-28 with the bound.
 #pragma once
@@ -106,7 +106,9 @@ struct ValueTile : RowTile<D, F8> {
 // NT: blocks of 8 query rows; a warp folds H 16-key tiles at a time.  Two tiles halve the waits and the
 // bookkeeping per key and give the products two independent chains (20 rows over e4m3 keys: 38.4 us with
 // one, 36.2 with two); the registers do not hold them with 32 rows, nor a warp's shared memory three
-// slots of them with bf16 rows of d = 128 (and 168 us are near the floor of 164 there).
+// slots of them with bf16 rows of d = 128 (and 166 us are near the floor of 164 there).  With 32 rows of
+// d = 128 they do not hold one tile's either: 80 (bf16) and 88 bytes (e4m3) of a thread are spilled, 62 and
+// 59 us for 64 x 8192 keys, where 24 rows take 55 and 43.
 template <int D, bool F8, int NT>
 struct AttnCfg {
     using K = KeyTile<D, F8>;
@@ -160,8 +162,8 @@ __device__ __forceinline__ void attn_finish(const PagedParams& p, size_t row, in
 // Joins the partial states of CTAs c0 .. c1 (first_slot, then 2c) into rows [row, row + rows), of which
 // this is one of `shares` CTAs.  `each` of the WARPS warps take ROWS rows together, every each-th state in order,
 // kBatch loaded together, and meet in shared memory (WARPS * ROWS * 33 float4).  Two rows together where
-// there may be more than 8 keep twice the loads in flight: 7 uneven sequences, 20 rows over e4m3 keys, 34.7 -> 32.8 us,
-// 4 x 32768 keys of bf16, 32 rows, 66.1 -> 60.8; up to 8 rows have a warp or more a row anyway.
+// there may be more than 8 keep twice the loads in flight: 7 uneven sequences, 20 rows over e4m3 keys, 34.7 -> 32.8 us
+// (33.5 with scores rounded once), 4 x 32768 keys of bf16, 32 rows, 66.1 -> 60.8; up to 8 rows have a warp or more a row anyway.
 constexpr int kBatch = 8;
 
 struct RowState {

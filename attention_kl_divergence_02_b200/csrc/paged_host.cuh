@@ -14,7 +14,8 @@ int page_shift_of(int n) {
     return s;
 }
 
-// Query rows are folded in blocks of 8 n.  Attention: n = 1 to 4, the fewest blocks that hold a KV head's rows.
+// Query rows are folded in blocks of 8 n.  Attention: n = 1 to 4, the fewest blocks that hold a KV head's rows (beyond
+// 32 rows, blocks of 32 and a rest in one of 32 too).
 // Divergence: 1 or 2; more rows are several blocks, which read the keys again, from L2, since the CTAs
 // that do the blocks of one head run side by side (32 rows over 64 x 8192 bf16 keys of d = 128: 52 us, and
 // 65 with one block of 32, whose query fragments do not fit the registers).
@@ -75,7 +76,8 @@ int launch_main(K kernel, int smem, const skl::PagedParams& p, cudaStream_t st, 
 // bf16 (e4m3), whole against shares, us: one sequence of 128 keys 4.1 against 5.8, 256 keys 5.4 against 5.9
 // (5.9 against 7.1), 512 keys 8.1 against 6.3 (8.1 against 7.1); 32 sequences of 512 keys 14.0 against 17.1
 // (9.7 against 12.7).  Units are 64 (128) keys.  With enough segments to fill half the grid, eight units
-// bound what uneven lengths can cost.
+// bound what uneven lengths can cost.  The host knows the table's width and not the lengths: behind a table that is
+// kept wider than the batch needs, as in a captured step, short sequences take the shares.
 template <int UNIT>
 void paged_grid(skl::PagedParams* p, int ctas) {
     const long long units = ((long long)p->width * p->page_size + UNIT - 1) / UNIT;
